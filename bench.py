@@ -233,10 +233,14 @@ def source_family(workload):
 PREFILL_SOURCES = ("qmv_prefill.cu", "qmv_prefill.h", "qmv_prefill_plan.h", "qmv_common.cuh", "qmv_launch.h")
 
 
+# The paged-cache calls' sources: no workload here launches them.
+CACHE_SOURCES = ("qmv_kv", "qmv_attn")
+
+
 def source_sha(family="decode"):
     """Hash of the kernel sources a traffic record depends on: the prefill
-    kernel's files, (decode) every other source of the library, or (all)
-    every source."""
+    kernel's files, (decode) every other source of the product calls, or (all)
+    every source of them."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "weight_quantized_decode_gb300", "csrc")
     for fn in sorted(os.listdir(csrc)):
@@ -245,7 +249,7 @@ def source_sha(family="decode"):
         if family == "prefill":
             if fn not in PREFILL_SOURCES:
                 continue
-        elif fn == "qmv_probe.cu" or (family == "decode" and fn in ("qmv_prefill.cu", "qmv_prefill_plan.h")):
+        elif fn == "qmv_probe.cu" or fn.startswith(CACHE_SOURCES) or (family == "decode" and fn in ("qmv_prefill.cu", "qmv_prefill_plan.h")):
             continue
         h.update(open(os.path.join(csrc, fn), "rb").read())
     return h.hexdigest()[:16]

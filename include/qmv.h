@@ -54,7 +54,7 @@
  *     asynchronous: they enqueue work on `stream` and return; the host never
  *     blocks (except qmv_device_status, which synchronises `stream`).
  *   - Argument errors are reported before anything is enqueued.  Errors found
- *     on the device (an expert index out of range) are recorded in a device
+ *     on the device (an expert index or a page out of range) are recorded in a device
  *     status word read by qmv_device_status(); the kernel never traps.
  *   - N == 0 or M == 0: nothing to do, QMV_OK, nothing enqueued.
  *     K == 0: y is filled with zeros (an empty sum).
@@ -99,6 +99,13 @@ typedef enum {
 /* Device status word bits (qmv_device_status). */
 #define QMV_DEV_BAD_EXPERT  0x1   /* an expert index was outside [0, n_experts) */
 #define QMV_DEV_TIMEOUT     0x2   /* a bounded wait in a kernel gave up          */
+#define QMV_DEV_BAD_PAGE    0x4   /* a page or slot outside the cache            */
+#define QMV_DEV_NO_PAGES    0x8   /* free list, table row or token outputs full  */
+#define QMV_DEV_BAD_LENGTH  0x10  /* a length, count or position out of range    */
+
+/* How a cache holds its rows (the `kind` of the paged-cache calls). */
+#define QMV_KV_F16  0   /* fp16 values                                           */
+#define QMV_KV_Q8   1   /* int8 codes c and one fp32 scale d to a row: y = c * d */
 
 /*
  * Q4_0 decode GEMV.  Prior art: the bakeoff's fused_q4 kernels (a warp per
@@ -339,6 +346,130 @@ QMV_API qmv_status qmm_q4_0_prefill(const void *W, const void *x, float *y,
  */
 QMV_API qmv_status qmm_q8_0_prefill(const void *W, const void *x, float *y,
                             int64_t N, int64_t K, int64_t M, qmv_stream_t stream);
+
+/*
+ * ---- The paged key/value cache -------------------------------------------------
+ *
+ * What a decoder keeps between its stacked query/key/value product and its
+ * output product, for steps of one token, of a tree of drafted tokens, or of a
+ * chunk of a prompt.  The three calls below share these layouts:
+ *
+ *   cache   : k and v are [n_pages][Hkv][page][D], rows of D values dense, fp16
+ *             or int8 (`kind`); page p begins page_stride elements after page
+ *             p - 1 (>= Hkv * page * D, so k and v may be interleaved page by
+ *             page in one buffer), a multiple of 16 bytes.  QMV_KV_Q8 adds
+ *             k_scale and v_scale, fp32 [n_pages][Hkv][page], dense.
+ *             page: a power of two, 16 .. 256.  D: 64 or 128.
+ *             n_pages * page < 2^31 (a slot is an int32: page id * page + row);
+ *             offsets in elements are 64-bit.
+ *   table   : int32 [R][width], the page ids of each of R requests in order.
+ *   start   : int32 [R + 1], offsets of each request's new tokens among the T
+ *             tokens of the step (start[0] = 0).
+ *   kv_len  : int32 [R], tokens of each request in the cache, the new ones
+ *             included: the new ones are its last places.
+ *   tree    : int32 [T][tree_words], or NULL for a chain.  Bit j % 32 of word
+ *             j / 32 of a token's row is set where the token sees node j of its
+ *             own request (j counts that request's new tokens).  Rows list a
+ *             node's ancestors and itself; any other pattern, an empty one too,
+ *             is taken as it stands.  Nodes past 32 * tree_words are unseen,
+ *             bits past a request's last new token are ignored.
+ * Arrays are 4-byte aligned, k, v, q, qkv, cos/sin tables and the workspace 16-byte.
+ * The contents of lengths, tables and slots are checked on the device: each
+ * declaration says what a bad one gives; nothing is read or written outside
+ * the arrays.  All calls are asynchronous on `stream`, can be captured in a
+ * graph (no size depends on device contents), and with programmatic dependent
+ * launch on wait for the previous kernel before they read anything.
+ */
+
+/*
+ * Page and slot maps of one step, from the requests' lengths.
+ *   len, n_new : int32 [R], tokens in the cache before the step, and new ones.
+ *   free_pages : int32 [n_free], ids of unused pages, taken in order from
+ *                index *head on (head NULL: 0); *head_out (may be NULL) is the
+ *                index after the last one taken.
+ *   table      : int32 [R][width]: entries [0, ceil(len / page)) are read, and
+ *                entries up to ceil((len + n_new) / page) are filled from the list.
+ *   Outputs: start [R + 1], kv_len [R], and to each of the T tokens slots
+ *   (cache slot), pos (len + i for the i-th new token; with a tree the depth:
+ *   len + number of nodes its row names - 1, not below len) and request.
+ *   Places of the T token outputs past the last new token get slot -1, pos 0
+ *   and request -1.
+ * Calling it again with the same inputs gives the same outputs.
+ * More than T new tokens: the ones past T are dropped (start and kv_len count
+ * the rest).  A list or table row that is too short: the slots without a page
+ * are -1, and so are the table entries.  Both set QMV_DEV_NO_PAGES.  A page id
+ * outside [0, n_pages): slot -1, QMV_DEV_BAD_PAGE.  A negative length or
+ * count, or a sum past 2^31 - 1: no new tokens, QMV_DEV_BAD_LENGTH.
+ * 0 <= R, T, n_free, width < 2^31.
+ */
+QMV_API qmv_status qmv_kv_pages(const int32_t *len, const int32_t *n_new, const int32_t *free_pages,
+                        int64_t n_free, const int32_t *head, const int32_t *tree, int64_t tree_words,
+                        int32_t *table, int32_t *start, int32_t *kv_len, int32_t *slots, int32_t *pos,
+                        int32_t *request, int32_t *head_out, int64_t R, int64_t width, int64_t page,
+                        int64_t n_pages, int64_t T, qmv_stream_t stream);
+
+/*
+ * Writes the key and value rows of T new tokens into the cache, rotated by
+ * their positions, and returns the rotated queries.
+ *   qkv   : [T][stride] fp32 (qkv_f32 != 0: what the decode calls return) or
+ *           fp16; the first (Hq + 2 Hkv) * D of a row are the query heads, the
+ *           key heads, the value heads.  stride in elements, a multiple of 4;
+ *           qkv 16-byte aligned (fp16: 8).
+ *   slots : int32 [T]; -1 writes no cache row (padding).  Slots of one call
+ *           must differ from each other.
+ *   rot   : the first `rot` values of each query and key head are rotated
+ *           (0 <= rot <= D, a multiple of 8; 0: no rotation, pos and the
+ *           tables may be NULL), in pairs (2i, 2i + 1) where `interleaved`,
+ *           else (i, i + rot / 2): (a, b) -> (a cos - b sin, b cos + a sin),
+ *           each product and sum rounded to fp32.
+ *   pos, cos_table, sin_table : int32 [T], fp32 [n_pos][rot / 2].
+ *   q     : fp16 [T][Hq][D], rounded once.  k, v: see the cache layout.
+ * An 8-bit row is d = max |y| / 127 (fp32) and codes round(y / d), ties away
+ * from zero (y times the rounded reciprocal of d); rows must be finite.
+ * A slot outside the cache other than -1 writes nothing (QMV_DEV_BAD_PAGE); a
+ * position outside [0, n_pos) gives a NaN query row and no cache row
+ * (QMV_DEV_BAD_LENGTH).
+ */
+QMV_API qmv_status qmv_kv_append(const void *qkv, int64_t stride, int qkv_f32, const int32_t *slots,
+                         const int32_t *pos, const float *cos_table, const float *sin_table, int64_t n_pos,
+                         int64_t rot, int interleaved, void *q, void *k, void *v, float *k_scale,
+                         float *v_scale, int kind, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                         int64_t n_pages, int64_t page, int64_t page_stride, qmv_stream_t stream);
+
+/*
+ * Bytes of workspace qmv_tree_attn takes on the current device, whatever the
+ * sizes of the call (-1 on a CUDA error).  The caller zeroes it once; every
+ * call leaves it ready for the next.  Calls that may run at the same time
+ * need a workspace each.
+ */
+QMV_API int64_t qmv_tree_attn_workspace(void);
+
+/*
+ * Attention of the step's tokens over the cache:
+ *     out[t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s_j = scale * q[t][h] . k_j
+ * over the places j that token t of request r sees: every place before the
+ * request's new tokens, and of those the nodes its tree row names (tree NULL:
+ * itself and the ones before it).  Query head h reads key/value head
+ * h / (Hq / Hkv).  A token that sees nothing gets zeros.  Values in places
+ * that a token does not see (stale rows past a request's end, infinities or
+ * NaN in nodes off its path) do not reach its output.
+ *   q     : fp16 [T][q_stride]: Hq heads of D; q_stride in elements, a
+ *           multiple of 8.  out: fp16 [T][Hq][D].
+ *   scale : HOST pointer to the softmax scale, read before the call returns
+ *           (NULL: 1 / sqrt(D)).
+ * Scores, maxima, sums and outputs are held in fp32; the weights p enter the
+ * value product rounded to fp16, and the output is rounded once.
+ * Rows of `out` past start[R] are left as they are.  A request whose page ids
+ * leave [0, n_pages), or whose kv_len is below its new tokens or above
+ * width * page, gets NaN (QMV_DEV_BAD_PAGE); other requests are unaffected.
+ * Hq a multiple of Hkv, 0 <= R <= 2^20, 0 <= T <= 2^24, T * Hq < 2^31.
+ */
+QMV_API qmv_status qmv_tree_attn(const void *q, int64_t q_stride, const void *k, const void *v,
+                         const float *k_scale, const float *v_scale, int kind, int64_t n_pages, int64_t page,
+                         int64_t page_stride, const int32_t *table, int64_t width, const int32_t *start,
+                         const int32_t *kv_len, const int32_t *tree, int64_t tree_words, const float *scale,
+                         void *out, void *workspace, int64_t workspace_bytes, int64_t R, int64_t T, int64_t Hq,
+                         int64_t Hkv, int64_t D, qmv_stream_t stream);
 
 /*
  * Reads and clears the device status word (QMV_DEV_* bits) of the current

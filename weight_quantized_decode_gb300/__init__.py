@@ -18,6 +18,11 @@ Functions (same names as the C ABI):
     qmv_moe(W_pool, expert_idx, n_experts, x, N, y=None, stream=None)
     qmm_q4_0_prefill(W, x, y=None, stream=None)  -> y fp32 [M, N]
     qmm_q8_0_prefill(W, x, y=None, stream=None)  -> y fp32 [M, N]
+    KvCache(k, v, k_scale=None, v_scale=None), qmv_kv_cache(...) -> a paged key/value cache (fp16 or int8 rows)
+    qmv_kv_pages(lens, n_new, free, table, page, tokens, ...) -> KvPages: start, kv_len, slots, pos, request, head
+    qmv_kv_append(qkv, cache, slots, n_heads, pos, cos, sin, ...) -> rotated q; k, v rows written to the cache
+    qmv_tree_attn(q, cache, table, start, kv_len, tree=None, ...) -> attention over the cache, fp16 [T, heads, D]
+    qmv_tree_attn_workspace(device=None)         -> the workspace a program keeps for qmv_tree_attn
     qmv_device_status(stream=None)               -> int (QMV_DEV_* bits, cleared)
     qmv_read_probe(buf, out=None, stream=None)   -> checksum tensor (read-only bandwidth probe)
     qmv_set_pdl(enable), qmv_status_str(code), qmv_version()
@@ -28,6 +33,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # QMV_LIB selects another build of the same library (the phase-timeline
@@ -37,6 +43,11 @@ LIB_PATH = os.environ.get("QMV_LIB") or os.path.join(_HERE, "libqmv.so")
 QMV_OK = 0
 QMV_DEV_BAD_EXPERT = 0x1
 QMV_DEV_TIMEOUT = 0x2
+QMV_DEV_BAD_PAGE = 0x4
+QMV_DEV_NO_PAGES = 0x8
+QMV_DEV_BAD_LENGTH = 0x10
+QMV_KV_F16 = 0
+QMV_KV_Q8 = 1
 Q4_0_BLOCK_BYTES = 18
 Q8_0_BLOCK_BYTES = 34
 Q2W_BLOCK_BYTES = 10
@@ -83,6 +94,16 @@ def lib():
         L.qmv_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         L.qmv_read_probe.restype = ctypes.c_int
         L.qmv_read_probe.argtypes = [vp, i64, vp, vp]
+        ci = ctypes.c_int
+        L.qmv_kv_pages.restype = ci
+        L.qmv_kv_pages.argtypes = [vp, vp, vp, i64, vp, vp, i64] + [vp] * 7 + [i64] * 5 + [vp]
+        L.qmv_kv_append.restype = ci
+        L.qmv_kv_append.argtypes = [vp, i64, ci, vp, vp, vp, vp, i64, i64, ci, vp, vp, vp, vp, vp, ci] + [i64] * 7 + [vp]
+        L.qmv_tree_attn_workspace.restype = i64
+        L.qmv_tree_attn_workspace.argtypes = []
+        L.qmv_tree_attn.restype = ci
+        L.qmv_tree_attn.argtypes = [vp, i64, vp, vp, vp, vp, ci, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp,
+                                    i64] + [i64] * 5 + [vp]
         L.qmv_set_pdl.restype = None
         L.qmv_set_pdl.argtypes = [ctypes.c_int]
         L.qmv_status_str.restype = ctypes.c_char_p
@@ -444,3 +465,206 @@ def qmv_device_status(stream=None) -> int:
     out = ctypes.c_int32(0)
     _check("qmv_device_status", lib().qmv_device_status(_stream_handle(stream), ctypes.byref(out)))
     return int(out.value)
+
+
+# -- the paged key/value cache ---------------------------------------------------------
+
+class KvCache:
+    """A paged key/value cache: k and v [n_pages, kv_heads, page, head_dim], fp16 or int8 (then with one fp32
+    scale to a row, k_scale and v_scale [n_pages, kv_heads, page]).  The rows of a page are dense; pages may lie
+    apart by any stride the two share (k and v interleaved in one buffer, for instance)."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads", "page", "head_dim", "kind", "device", "_args")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        torch = _torch()
+        if not (k.is_cuda and v.is_cuda):
+            raise TypeError("KvCache: k and v must be CUDA tensors (no CPU path)")
+        if k.dtype != v.dtype or k.dtype not in (torch.float16, torch.int8):
+            raise TypeError("KvCache: k and v must both be float16 or int8")
+        if k.dim() != 4 or k.shape != v.shape or k.device != v.device:
+            raise ValueError("KvCache: k and v must be [n_pages, kv_heads, page, head_dim] on one device")
+        n_pages, heads, page, dim = k.shape
+        dense = (page * dim, dim, 1)
+        if tuple(k.stride()[1:]) != dense or tuple(v.stride()[1:]) != dense or (n_pages > 1 and k.stride(0) != v.stride(0)):
+            raise ValueError("KvCache: the rows of a page must be dense, and k and v have one page stride")
+        self.kind = QMV_KV_F16 if k.dtype == torch.float16 else QMV_KV_Q8
+        for s in (k_scale, v_scale):
+            if (self.kind == QMV_KV_Q8) != (s is not None):
+                raise ValueError("KvCache: an int8 cache has k_scale and v_scale, a float16 cache has none")
+            if s is not None and not (s.is_cuda and s.device == k.device and s.dtype == torch.float32
+                                      and s.is_contiguous() and tuple(s.shape) == (n_pages, heads, page)):
+                raise ValueError("KvCache: scales must be contiguous float32 [n_pages, kv_heads, page] beside k and v")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.kv_heads, self.page, self.head_dim = n_pages, heads, page, dim
+        self.device = k.device
+        stride = k.stride(0) if n_pages > 1 else heads * page * dim
+        self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else 0,
+                      v_scale.data_ptr() if v_scale is not None else 0, stride)
+
+
+def qmv_kv_cache(n_pages, kv_heads, page, head_dim, dtype=None, device="cuda"):
+    """A KvCache of zeros: dtype torch.float16 (default) or torch.int8 (8-bit codes with a scale to a row)."""
+    torch = _torch()
+    dtype = torch.float16 if dtype is None else dtype
+    shape = (n_pages, kv_heads, page, head_dim)
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.int8:
+        return KvCache(k, v)
+    return KvCache(k, v, *(torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+class KvPages(NamedTuple):
+    """The maps of one step (qmv_kv_pages): int32 CUDA tensors."""
+    start: object      # [R + 1] offsets of the requests' new tokens
+    kv_len: object     # [R] tokens in the cache, the new ones included
+    slots: object      # [tokens] cache slot of each new token, -1 for padding
+    pos: object        # [tokens] position (depth in the tree, with one)
+    request: object    # [tokens] request, -1 for padding
+    head: object       # [1] index in the free list after the last page taken
+
+
+def _int32(fn, name, t, dim):
+    torch = _torch()
+    if not t.is_cuda:
+        raise TypeError(f"{fn}: {name} must be a CUDA tensor (no CPU path)")
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+        raise TypeError(f"{fn}: {name} must be a contiguous int32 tensor with {dim} dimension" + ("s" if dim > 1 else ""))
+    return t.data_ptr()
+
+
+def _tree_args(fn, tree, tokens):
+    """(address, words) of a tree mask [tokens, words], (0, 0) for none."""
+    if tree is None:
+        return 0, 0
+    ptr = _int32(fn, "tree", tree, 2)
+    if tree.shape[0] != tokens or (tree.shape[1] == 0 and tokens > 0):
+        raise ValueError(f"{fn}: tree must have a row of at least one word for each of the {tokens} tokens")
+    return ptr, tree.shape[1]
+
+
+def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n_pages=None, stream=None):
+    """Page and slot maps of one step, on the GPU.  lens, n_new [R]; free [n], ids of unused pages, taken in order
+    from index `head` ([1], default 0) on; table [R, width] is completed in place; tokens: length of the per-token
+    outputs (what the new tokens leave over is padding); tree [tokens, words]: positions are depths.  n_pages: size
+    of the cache, to refuse wrong page ids (default: any that a slot can hold).  Returns KvPages."""
+    torch = _torch()
+    fn = "qmv_kv_pages"
+    a = [_int32(fn, "lens", lens, 1), _int32(fn, "n_new", n_new, 1), _int32(fn, "free", free, 1),
+         _int32(fn, "table", table, 2)]
+    R, tokens, page = lens.shape[0], int(tokens), int(page)
+    if n_new.shape[0] != R or table.shape[0] != R:
+        raise ValueError(f"{fn}: lens, n_new and table must have one row to a request")
+    if tokens < 0 or page <= 0:
+        raise ValueError(f"{fn}: tokens must not be negative, page must be positive")
+    head_ptr = 0 if head is None else _int32(fn, "head", head, 1)
+    if head is not None and head.shape[0] != 1:
+        raise ValueError(f"{fn}: head must be one number")
+    tree_ptr, words = _tree_args(fn, tree, tokens)
+    others = [t for t in (n_new, free, table, head, tree) if t is not None]
+    with _on_device(fn, lens, *others):
+        out = torch.empty(2 * R + 2 + 3 * tokens, dtype=torch.int32, device=lens.device)
+        got = KvPages(*out.split((R + 1, R, tokens, tokens, tokens, 1)))
+        o, n = out.data_ptr(), 4 * tokens
+        s = o + 4 * (2 * R + 1)
+        _check(fn, lib().qmv_kv_pages(a[0], a[1], a[2], free.shape[0], head_ptr, tree_ptr, words, a[3], o,
+                                      o + 4 * (R + 1), s, s + n, s + 2 * n, s + 3 * n, R, table.shape[1], page,
+                                      (0x7fffffff // page) if n_pages is None else int(n_pages), tokens,
+                                      _stream_handle(stream)))
+    return got
+
+
+def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, interleaved=False, q=None, stream=None):
+    """Writes the key and value rows of qkv [T, (n_heads + 2 kv_heads) * D] (fp32 or fp16, rows any multiple of four
+    values apart) to the cache at slots [T], rotated by rows pos [T] of the tables cos, sin [positions, rot / 2]
+    (None: not rotated); returns the rotated queries, fp16 [T, n_heads, D]."""
+    torch = _torch()
+    fn = "qmv_kv_append"
+    if not qkv.is_cuda:
+        raise TypeError(f"{fn}: qkv must be a CUDA tensor (no CPU path)")
+    if qkv.dtype not in (torch.float32, torch.float16):
+        raise TypeError(f"{fn}: qkv must be float32 or float16")
+    T, hk, D = qkv.shape[0], cache.kv_heads, cache.head_dim
+    if qkv.dim() != 2 or qkv.shape[1] != (n_heads + 2 * hk) * D or (T and qkv.stride(1) != 1):
+        raise ValueError(f"{fn}: qkv must be [T, (n_heads + 2 * {hk}) * {D}] with dense rows")
+    slots_ptr = _int32(fn, "slots", slots, 1)
+    if slots.shape[0] != T:
+        raise ValueError(f"{fn}: one slot to a token")
+    others = [slots, cache.k]
+    pos_ptr = cos_ptr = sin_ptr = n_pos = rot = 0
+    if (cos is None) != (sin is None) or (cos is not None and pos is None):
+        raise ValueError(f"{fn}: a rotation takes pos, cos and sin")
+    if cos is not None:
+        pos_ptr = _int32(fn, "pos", pos, 1)
+        if pos.shape[0] != T:
+            raise ValueError(f"{fn}: one position to a token")
+        if not (cos.is_cuda and sin.is_cuda and cos.dtype == sin.dtype == torch.float32 and cos.dim() == 2
+                and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError(f"{fn}: cos and sin must be contiguous CUDA float32 [positions, rot / 2]")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
+        others += [pos, cos, sin]
+    if q is None:
+        q = torch.empty((T, n_heads, D), dtype=torch.float16, device=qkv.device)
+    elif not (q.is_cuda and q.dtype == torch.float16 and q.is_contiguous() and q.numel() == T * n_heads * D):
+        raise ValueError(f"{fn}: q must be a contiguous CUDA float16 tensor of {T}x{n_heads}x{D}")
+    k, v, ks, vs, page_stride = cache._args
+    with _on_device(fn, qkv, q, *others):
+        _check(fn, lib().qmv_kv_append(qkv.data_ptr(), qkv.stride(0) if T > 1 else qkv.shape[1],
+                                       qkv.dtype == torch.float32, slots_ptr, pos_ptr, cos_ptr, sin_ptr, n_pos, rot,
+                                       bool(interleaved), q.data_ptr(), k, v, ks, vs, cache.kind, T, int(n_heads), hk,
+                                       D, cache.n_pages, cache.page, page_stride, _stream_handle(stream)))
+    return q
+
+
+def qmv_tree_attn_workspace(device=None):
+    """The workspace of qmv_tree_attn: kept by a program from call to call, one for each stream that may run at the
+    same time as another."""
+    torch = _torch()
+    device = torch.device("cuda" if device is None else device)
+    with torch.cuda.device(device):
+        n = lib().qmv_tree_attn_workspace()
+        if n < 0:
+            raise QmvError("qmv_tree_attn_workspace", 6)
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=None, workspace=None, stream=None):
+    """Attention of new tokens over the cache: q fp16 [T, heads, D] (rows any multiple of eight values apart), table
+    [R, width], start [R + 1], kv_len [R] (new tokens included), tree [T, words] (None: a chain), scale (None:
+    1 / sqrt(D)), workspace as qmv_tree_attn_workspace gives it (None: one is made for this call).
+    Returns fp16 [T, heads, D]."""
+    torch = _torch()
+    fn = "qmv_tree_attn"
+    if not q.is_cuda:
+        raise TypeError(f"{fn}: q must be a CUDA tensor (no CPU path)")
+    if q.dtype != torch.float16:
+        raise TypeError(f"{fn}: q must be float16")
+    D = cache.head_dim
+    if q.dim() != 3 or q.shape[2] != D or (q.numel() and (q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != D))):
+        raise ValueError(f"{fn}: q must be [T, heads, {D}] with dense rows")
+    T, H = q.shape[:2]
+    R = kv_len.shape[0]
+    a = [_int32(fn, "table", table, 2), _int32(fn, "start", start, 1), _int32(fn, "kv_len", kv_len, 1)]
+    if table.shape[0] != R or start.shape[0] != R + 1:
+        raise ValueError(f"{fn}: table [R, width], start [R + 1] and kv_len [R] must agree")
+    tree_ptr, words = _tree_args(fn, tree, T)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+    elif not (out.is_cuda and out.dtype == torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
+        raise ValueError(f"{fn}: out must be a contiguous CUDA float16 tensor of {T}x{H}x{D}")
+    if workspace is None:
+        workspace = qmv_tree_attn_workspace(q.device)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
+    others = [cache.k, table, start, kv_len, out, workspace] + ([tree] if tree is not None else [])
+    k, v, ks, vs, page_stride = cache._args
+    with _on_device(fn, q, *others):
+        _check(fn, lib().qmv_tree_attn(q.data_ptr(), q.stride(0) if T > 1 else H * D, k, v, ks, vs, cache.kind,
+                                       cache.n_pages, cache.page, page_stride, a[0], table.shape[1], a[1], a[2],
+                                       tree_ptr, words,
+                                       None if scale is None else ctypes.byref(ctypes.c_float(scale)),
+                                       out.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), R, T, H, cache.kv_heads, D,
+                                       _stream_handle(stream)))
+    return out

@@ -10,6 +10,7 @@
 
 #include "../../include/qmv.h"
 #include "qmv_gemv.cuh"
+#include "qmv_kv.h"
 #include "qmv_launch.h"
 #include "qmv_prefill.h"
 #include "qmv_tune_table.h"
@@ -472,6 +473,15 @@ qmv_status check_common(const void *W, const void *x, float *y, int64_t N, int64
 }
 
 }  // namespace
+
+cudaError_t call_env(int **status, int *sms, bool *pdl)
+{
+    int dev = 0, optin = 0;
+    cudaError_t e = current_device(&dev);
+    if (e != cudaSuccess) return e;
+    *pdl = g_pdl.load(std::memory_order_relaxed) != 0;
+    return device_info(dev, status, sms, &optin);
+}
 
 cudaError_t ensure_smem_optin(const void *func, size_t smem)
 {
