@@ -373,7 +373,8 @@ QMV_API qmv_status qmm_q8_0_prefill(const void *W, const void *x, float *y,
  *             node's ancestors and itself; any other pattern, an empty one too,
  *             is taken as it stands.  Nodes past 32 * tree_words are unseen,
  *             bits past a request's last new token are ignored.
- * Arrays are 4-byte aligned, k, v, q, qkv, cos/sin tables and the workspace 16-byte.
+ * Arrays of int32 are 4-byte aligned; k, v, scales, q, qkv, the cos / sin
+ * tables, out and the workspace 16-byte.
  * The contents of lengths, tables and slots are checked on the device: each
  * declaration says what a bad one gives; nothing is read or written outside
  * the arrays.  All calls are asynchronous on `stream`, can be captured in a

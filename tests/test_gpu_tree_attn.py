@@ -321,6 +321,8 @@ def test_refusals(q, ws):
         q.qmv_tree_attn(qd[:, :3], c, t, s, n, **ok)                   # heads not a multiple of kv heads
     with pytest.raises(q.QmvError):
         q.qmv_tree_attn(qd, c, t, s, n, scale=float("nan"), **ok)
+    with pytest.raises(q.QmvError):                                    # a workspace that is too small
+        q.qmv_tree_attn(qd, c, t, s, n, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     c48 = q.qmv_kv_cache(4, 2, 48, 64)
     with pytest.raises(q.QmvError):
         q.qmv_tree_attn(qd, c48, t, s, n, **ok)                        # page size

@@ -28,7 +28,7 @@ qmv_status check_cache(int64_t n_pages, int64_t Hkv, int64_t page, int64_t D, in
     if (page_shift_of(page) < 0 || (D != 64 && D != 128) || Hkv < 1 || Hkv > 1024) return QMV_ERR_SHAPE;
     if (n_pages < 1 || n_pages * page > kInt32Max) return QMV_ERR_SHAPE;
     if (kind != QMV_KV_F16 && kind != QMV_KV_Q8) return QMV_ERR_SHAPE;
-    if (page_stride < Hkv * page * D || page_stride > (int64_t(1) << 39)) return QMV_ERR_SHAPE;
+    if (page_stride < Hkv * page * D || page_stride > (int64_t(1) << 38)) return QMV_ERR_SHAPE;
     // 16-byte rows of every page: the strides the copies need
     if ((page_stride * (kind == QMV_KV_F16 ? 2 : 1)) % 16 != 0) return QMV_ERR_ALIGN;
     return QMV_OK;
@@ -111,7 +111,7 @@ qmv_status qmv_kv_append(const void *qkv, int64_t stride, int qkv_f32, const int
         return QMV_ERR_NULL;
     if (!aligned(qkv, qkv_f32 ? 16 : 8) || stride % 4 != 0 || !aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) ||
         !aligned(slots, 4) || !aligned(pos, 4) || !aligned(cos_table, 16) || !aligned(sin_table, 16) ||
-        !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        !aligned(k_scale, 16) || !aligned(v_scale, 16))
         return QMV_ERR_ALIGN;
     AppendParams p = {};
     int sms = 0;
@@ -175,7 +175,7 @@ qmv_status qmv_tree_attn(const void *q, int64_t q_stride, const void *k, const v
         return QMV_ERR_NULL;
     if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
         !aligned(table, 4) || !aligned(start, 4) || !aligned(kv_len, 4) || !aligned(tree, 4) ||
-        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(workspace, 16))
+        !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(workspace, 16))
         return QMV_ERR_ALIGN;
     AttnParams p = {};
     int sms = 0;
