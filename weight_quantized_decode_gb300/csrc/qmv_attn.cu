@@ -1,0 +1,66 @@
+// qmv_attn.cu -- attention over the paged cache, host side: which kernel a call
+// runs on, the tensor maps of the cache, the workspace.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "qmv_attn.cuh"
+
+namespace qmv {
+
+namespace {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+}  // namespace
+
+bool encode_rows(CUtensorMap *map, const AttnParams &p, const void *base, int D, int kind, int rows)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const int esz = kind == kKvF16 ? 2 : 1;
+    const int inner = D * esz < 128 ? D : 128 / esz;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.Hkv) << p.page_shift,
+                                static_cast<cuuint64_t>(p.n_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D * esz), static_cast<cuuint64_t>(p.page_stride) * esz};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, kind == kKvF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               inner * esz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t tree_attn_workspace_bytes(int sms)
+{
+    const int64_t a = attn_rows_workspace_floats(sms), b = attn_tiles_workspace_floats(sms);
+    return 4 * (kMaxGrid + (a > b ? a : b));
+}
+
+cudaError_t launch_tree_attn(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl)
+{
+    // Rows that share a key/value head in the average request: up to 16 fill
+    // one tile of the streaming kernel; more go to the 128-row tiles.
+    const int64_t rows = (p.T + p.R - 1) / p.R * p.group;
+    if (rows <= 16 || kind == kKvQ8) return launch_attn_rows(p, D, kind, sms, s, pdl);
+    return launch_attn_tiles(p, D, kind, sms, s, pdl);
+}
+
+}  // namespace qmv

@@ -14,6 +14,8 @@
 // not depend on which one it was.
 #pragma once
 
+#include <cuda.h>
+
 #include <cstdint>
 
 #include "qmv_common.cuh"
@@ -23,15 +25,29 @@ namespace qmv {
 
 // Request r's share of the work.
 struct RequestWork {
-    int nodes;       // new tokens
-    int tiles;       // row tiles
-    int64_t len;     // places
-    int64_t blocks;  // blocks of one unit
-    bool bad;        // a length the cache cannot have: one block that gives NaN
-    int64_t total;   // blocks of all its units
+    int nodes;         // new tokens
+    int tiles;         // row tiles
+    int64_t len;       // places
+    bool bad;          // a length the cache cannot have: one block that gives NaN
+    int64_t per_head;  // blocks of the units of one key/value head
+    int64_t total;     // blocks of all its units
 };
 
-template <int ROWS, int BLOCK>
+// Blocks of the unit of row tile `tile`.  CUT: the rows of a chain see nothing
+// past the tile's last token, and the blocks there are left out.
+template <int ROWS, int BLOCK, bool CUT>
+__device__ __forceinline__ int64_t unit_blocks(const AttnParams &p, const RequestWork &w, int tile)
+{
+    if (w.bad) return 1;
+    int64_t places = w.len;
+    if (CUT && !p.tree) {
+        const int64_t last = ((static_cast<int64_t>(tile) + 1) * ROWS - 1) / p.group;   // the tile's last token
+        if (last < w.nodes) places = w.len - w.nodes + last + 1;
+    }
+    return (places + BLOCK - 1) / BLOCK;
+}
+
+template <int ROWS, int BLOCK, bool CUT>
 __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t r)
 {
     RequestWork w;
@@ -43,8 +59,13 @@ __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t
     w.bad = lo < 0 || hi > p.T || w.len < w.nodes || w.len > (p.width << p.page_shift);
     if (w.bad) w.len = 0;
     w.tiles = static_cast<int>((static_cast<int64_t>(w.nodes) * p.group + ROWS - 1) / ROWS);
-    w.blocks = w.bad ? 1 : (w.len + BLOCK - 1) / BLOCK;
-    w.total = static_cast<int64_t>(w.tiles) * p.Hkv * w.blocks;
+    if (CUT && !p.tree) {
+        w.per_head = 0;
+        for (int t = 0; t < w.tiles; ++t) w.per_head += unit_blocks<ROWS, BLOCK, CUT>(p, w, t);
+    } else {
+        w.per_head = w.tiles * unit_blocks<ROWS, BLOCK, CUT>(p, w, 0);
+    }
+    w.total = w.per_head * p.Hkv;
     return w;
 }
 
@@ -60,7 +81,7 @@ struct Share {
 };
 
 // Every thread of the block calls this (THREADS of them, a multiple of 32).
-template <int ROWS, int BLOCK, int THREADS>
+template <int ROWS, int BLOCK, bool CUT, int THREADS>
 __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
 {
     constexpr int W = THREADS / 32;
@@ -84,14 +105,14 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
         return v + add;
     };
     int64_t mine = 0, total = 0;
-    for (int64_t r = tid; r < p.R; r += THREADS) mine += request_work<ROWS, BLOCK>(p, r).total;
+    for (int64_t r = tid; r < p.R; r += THREADS) mine += request_work<ROWS, BLOCK, CUT>(p, r).total;
     scan(mine, &total);
     const int64_t g = total < gridDim.x ? total : static_cast<int64_t>(gridDim.x);
     const int64_t lo = g > 0 && blockIdx.x < g ? total * blockIdx.x / g : 0;
     const int64_t hi = g > 0 && blockIdx.x < g ? total * (blockIdx.x + 1) / g : 0;
     int64_t before = 0;
     for (int64_t r0 = 0; r0 < p.R && before <= lo && lo < hi; r0 += THREADS) {
-        const int64_t cnt = r0 + tid < p.R ? request_work<ROWS, BLOCK>(p, r0 + tid).total : 0;
+        const int64_t cnt = r0 + tid < p.R ? request_work<ROWS, BLOCK, CUT>(p, r0 + tid).total : 0;
         int64_t all = 0;
         const int64_t upto = before + scan(cnt, &all);
         if (cnt > 0 && upto - cnt <= lo && lo < upto) {
@@ -119,36 +140,55 @@ struct Segment {
     int64_t r;            // request
     int kvh, tile;        // key/value head, row tile
     int64_t b0, nb;       // its blocks [b0, b0 + nb) of the unit
+    int64_t blocks;       // blocks of the unit
     int64_t unit_first;   // the list's index of the unit's first block
     RequestWork w;
 };
 
-// Walks a CTA's segments.  Any number of threads may each keep one.
-template <int ROWS, int BLOCK>
+// Walks a CTA's segments (begin, then next until it is false).  Any number of
+// threads may each keep one.
+template <int ROWS, int BLOCK, bool CUT>
 struct SegmentWalk {
-    const AttnParams &p;
-    int64_t at, hi, r, before;
-    RequestWork w;
-    __device__ __forceinline__ SegmentWalk(const AttnParams &p_, const Share &sh)
-        : p(p_), at(sh.lo), hi(sh.hi), r(sh.r), before(sh.before)
+    int64_t at, hi;
+    Segment u;            // the unit that `at` falls into (b0, nb unused)
+    __device__ __forceinline__ void begin(const AttnParams &p, const Share &sh)
     {
-        if (at < hi) w = request_work<ROWS, BLOCK>(p, r);
+        at = sh.lo;
+        hi = sh.hi;
+        if (at >= hi) return;
+        u.r = sh.r;
+        u.w = request_work<ROWS, BLOCK, CUT>(p, u.r);
+        u.kvh = static_cast<int>((at - sh.before) / u.w.per_head);
+        u.unit_first = sh.before + u.kvh * u.w.per_head;
+        u.tile = 0;
+        u.blocks = unit_blocks<ROWS, BLOCK, CUT>(p, u.w, 0);
+        if (!CUT) {   // units of one size
+            u.tile = static_cast<int>((at - u.unit_first) / u.blocks);
+            u.unit_first += u.tile * u.blocks;
+        }
+        while (at >= u.unit_first + u.blocks) step(p);
     }
-    __device__ __forceinline__ bool next(Segment &s)
+    // To the unit that follows.
+    __device__ __forceinline__ void step(const AttnParams &p)
+    {
+        u.unit_first += u.blocks;
+        if (++u.tile == u.w.tiles) {
+            u.tile = 0;
+            if (++u.kvh == p.Hkv) {
+                u.kvh = 0;
+                do u.w = request_work<ROWS, BLOCK, CUT>(p, ++u.r);
+                while (u.w.total == 0);
+            }
+        }
+        u.blocks = unit_blocks<ROWS, BLOCK, CUT>(p, u.w, u.tile);
+    }
+    __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
     {
         if (at >= hi) return false;
-        while (at >= before + w.total) {
-            before += w.total;
-            w = request_work<ROWS, BLOCK>(p, ++r);
-        }
-        const int64_t unit = (at - before) / w.blocks;
-        s.r = r;
-        s.w = w;
-        s.kvh = static_cast<int>(unit / w.tiles);
-        s.tile = static_cast<int>(unit - static_cast<int64_t>(s.kvh) * w.tiles);
-        s.unit_first = before + unit * w.blocks;
-        s.b0 = at - s.unit_first;
-        s.nb = w.blocks - s.b0 < hi - at ? w.blocks - s.b0 : hi - at;
+        if (at >= u.unit_first + u.blocks) step(p);
+        s = u;
+        s.b0 = at - u.unit_first;
+        s.nb = u.blocks - s.b0 < hi - at ? u.blocks - s.b0 : hi - at;
         at += s.nb;
         return true;
     }
@@ -186,6 +226,35 @@ __device__ __forceinline__ uint32_t seen_places(const int32_t *tree_row, int tre
     return m & there;
 }
 
+// Bounded wait that also gives up when another role of the CTA has.
+__device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) return true;
+        if (*gave_up) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *gave_up = 1;
+            atomicOr(status, kDevTimeout);
+            return false;
+        }
+    }
+}
+
+// The same for a whole warp: every lane calls it and gets the same answer.
+__device__ __forceinline__ bool warp_wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = wait_or_give_up(bar, parity, gave_up, status);
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (ok)   // the phase has completed: every lane observes it before going on
+        while (!mbar_try_wait(bar, parity)) {
+        }
+    return ok;
+}
+
 // 2^x (the hardware's approximation; 2^-inf = 0).
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -207,8 +276,7 @@ __device__ __forceinline__ float *workspace_partial(const AttnParams &p, int cta
            (2 * static_cast<int64_t>(cta) + which) * partial_floats(rows, D);
 }
 
-// Writes `n` (a multiple of 8) values of row `row` of a segment's unit from
-// column d on, times `inv`, as fp16.
+// The output row of row `row` of a segment's unit.
 template <int ROWS, int D>
 __device__ __forceinline__ __half *out_row(const AttnParams &p, const Segment &s, int row)
 {
@@ -262,5 +330,27 @@ __device__ __forceinline__ void join_parts(const AttnParams &p, const Segment &s
         store_half8(out_row<ROWS, D>(p, s, row) + d, o);
     }
 }
+
+// Tensor copy of one box of cached rows: x the first column, y the row within
+// the page, z the page.
+__device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Tensor map of a cache's rows: [n_pages][Hkv * page][D], boxes of `rows` rows
+// and up to 128 bytes, swizzled over that width.  False where the driver has
+// no such call or refuses the shape.
+bool encode_rows(CUtensorMap *map, const AttnParams &p, const void *base, int D, int kind, int rows);
+
+// The two kernels' launches (qmv_attn_rows.cu, qmv_attn_tiles.cu) and the
+// workspace each needs.
+cudaError_t launch_attn_rows(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl);
+cudaError_t launch_attn_tiles(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl);
+int64_t attn_rows_workspace_floats(int sms);
+int64_t attn_tiles_workspace_floats(int sms);
 
 }  // namespace qmv

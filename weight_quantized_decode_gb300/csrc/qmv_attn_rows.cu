@@ -16,10 +16,7 @@
 // multiplies the score, the value scale the weight, both in fp32; weights are
 // held below fp16's largest value by a running power of two of the largest
 // value scale, handled like the running maximum.
-#include <cuda.h>
-
 #include <cstdint>
-#include <mutex>
 
 #include "qmv_attn.cuh"
 #include "qmv_launch.h"
@@ -84,14 +81,6 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t flipped, uint32_t se
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ float quad_max(float v)
 {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -135,14 +124,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     pdl_allow_next_grid();
     pdl_wait_prior_grid();
-    find_share<kRows, kBlock, kThreads>(p, &sh);
+    find_share<kRows, kBlock, false, kThreads>(p, &sh);
 
-    SegmentWalk<kRows, kBlock> walk(p, sh);
+    SegmentWalk<kRows, kBlock, false> walk;
+    walk.begin(p, sh);
     Segment seg;
     uint32_t entry = 0;       // ring entries consumed so far, this warp's
     uint32_t asked = 0;       // entries requested so far
     bool gave_up = false;     // a wait ran out: nothing more is requested, outputs become NaN
-    while (walk.next(seg)) {
+    while (walk.next(p, seg)) {
         const int64_t len = seg.w.len;
         const int nodes = seg.w.nodes;
         const int64_t first_place = seg.b0 * kBlock + warp * kStep;
@@ -524,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         __syncthreads();
-        const bool whole = seg.nb == seg.w.blocks;
+        const bool whole = seg.nb == seg.blocks;
         const int first = whole ? 0 : owner_of(seg.unit_first, sh);
-        const int last = whole ? 0 : owner_of(seg.unit_first + seg.w.blocks - 1, sh);
+        const int last = whole ? 0 : owner_of(seg.unit_first + seg.blocks - 1, sh);
         float *part = whole ? nullptr : workspace_partial(p, blockIdx.x, seg.b0 == 0 ? 1 : 0, kRows, D);
         for (int i = tid; i < valid * (D / 8); i += kThreads) {
             const int row = i / (D / 8), d = (i - row * (D / 8)) * 8;
@@ -579,44 +569,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_wait_bounded(&bar[n % R::kSlots], (n / R::kSlots) & 1u, nullptr);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    });
-    return fn;
-}
-
-// Tensor map of a cache's rows: [n_pages][Hkv * page][D], boxes of `rows` rows
-// and up to 128 bytes, swizzled over that width.
-bool encode_rows(CUtensorMap *map, const AttnParams &p, const void *base, int D, int kind, int rows)
-{
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    const int esz = kind == kKvF16 ? 2 : 1;
-    const int inner = D * esz < 128 ? D : 128 / esz;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.Hkv) << p.page_shift,
-                                static_cast<cuuint64_t>(p.n_pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D * esz), static_cast<cuuint64_t>(p.page_stride) * esz};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(rows), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, kind == kKvF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               inner * esz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int KIND>
 cudaError_t launch_with(const AttnParams &p, int sms, cudaStream_t s, bool pdl)
 {
@@ -634,12 +586,9 @@ cudaError_t launch_with(const AttnParams &p, int sms, cudaStream_t s, bool pdl)
 
 }  // namespace
 
-int64_t tree_attn_workspace_bytes(int sms)
-{
-    return 4 * (kMaxGrid + 2 * (2 * static_cast<int64_t>(sms)) * partial_floats(kRows, 128));
-}
+int64_t attn_rows_workspace_floats(int sms) { return 2 * (2 * static_cast<int64_t>(sms)) * partial_floats(kRows, 128); }
 
-cudaError_t launch_tree_attn(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl)
+cudaError_t launch_attn_rows(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl)
 {
     if (2 * sms > kMaxGrid) return cudaErrorInvalidConfiguration;
     if (D == 64)

@@ -1,0 +1,741 @@
+// qmv_attn_tiles.cu -- attention over the paged cache for many query rows to a
+// key/value head (trees of drafted tokens, chunks of prompts): 128-row tiles on
+// the 5th-generation tensor cores (tcgen05.mma), scores and outputs in tensor
+// memory.
+//
+// A CTA (one to an SM) works on up to 256 rows of one (request, key/value
+// head) as two streams, each with a softmax warpgroup, a 128 x 128 score tile
+// and a 128 x D output in tensor memory:
+//   * more than 128 rows: a stream to each 128-row tile, both over every block
+//     of 128 places, so that a block is read once for 256 rows;
+//   * up to 128 rows: both streams hold the same rows, one takes the even and
+//     one the odd blocks, and their outputs are joined at the end of a segment.
+// While one stream's scores go through its softmax, the other's products run.
+//   s = q k^T: queries and keys from shared memory (K-major, 128-byte swizzle,
+// as the tensor copies deliver them).  The weights p go back to tensor memory
+// over the scores they came from, as fp16, and are the A operand of o += p v;
+// values are read N-major from the same kind of tile.  A thread owns a row: its
+// maximum and sum need no exchange.  The output in tensor memory is rescaled
+// only where a row's maximum has risen by more than 2^5 since it last was; until
+// then the weights simply come out larger, p <= 2^(10 + 5) < 65504.
+//   Warps: 0-3 and 4-7 the two softmax groups, 8 issues the products, 9 the
+// copies.  All waits are bounded.
+#include <cstdint>
+
+#include "qmv_attn.cuh"
+#include "qmv_launch.h"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kTile = 128;           // rows of a stream
+constexpr int kRows = 2 * kTile;     // rows of a unit
+constexpr int kBlock = 128;          // places of a block
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kThreads = 384;        // three warpgroups; warps 10 and 11 have nothing to do
+// Registers of a thread: at launch, and after the softmax groups have taken
+// what the others give up (the shares add up to the launch's).
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
+static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "shares of the launch's registers");
+constexpr float kShift = 10.0f;      // weights are 2^10 times exp(s - max)
+constexpr float kLazy = 5.0f;        // a maximum may lag this far (log2)
+
+template <int D>
+struct Ring {
+    static constexpr int kHalves = D / 64;                      // 64-column halves of a tile
+    static constexpr int kHalfBytes = kBlock * 128;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;     // 128 rows of fp16
+    static constexpr int kSlots = D == 128 ? 4 : 8;             // 128 KB of keys and values
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(2 + kSlots) * kTileBytes;
+};
+
+// ---- tensor memory and products -----------------------------------------------
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of this thread's lane; the values are there after ld_wait.
+__device__ __forceinline__ void ld_32cols(uint32_t taddr, uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+
+// The wait names the registers it makes valid, so that no use moves before it.
+__device__ __forceinline__ void ld_wait(uint32_t *v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_32cols(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+          "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]),
+          "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void st_16cols(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptors, 128-byte swizzle.  Rows of 128 bytes, eight
+// of them to a swizzle atom of 1024 bytes.  K-major (queries, keys): the row is
+// an M or N index, atoms follow each other along it.  N-major (values): the row
+// is a K index and carries 64 columns; `next64` bytes lead to the next 64.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t next64)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | static_cast<uint64_t>((next64 >> 4) & 0x3FFF) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+// Instruction descriptor, kind::f16: fp16 operands, fp32 accumulator, M = 128.
+__device__ __forceinline__ constexpr uint32_t mma_desc(int n, bool b_n_major)
+{
+    return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kTile >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(add ? 1 : 0)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(add ? 1 : 0)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Barrier `id` among `n` threads; the OR of their flags.
+__device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool group_or(int id, int n, bool flag)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(n), "r"(flag ? 1 : 0)
+        : "memory");
+    return r != 0;
+}
+
+// Order of a segment's tiles in the ring: step i asks for the values of block
+// i - lag and the keys of block i (lag 1: both streams on every block; 2: a
+// stream on every second one).
+__device__ __forceinline__ uint32_t seq_k(int i, int lag) { return static_cast<uint32_t>(i + (i >= lag ? i - lag + 1 : 0)); }
+__device__ __forceinline__ uint32_t seq_v(int i, int lag, int nb)
+{
+    return static_cast<uint32_t>(i + (i + lag < nb ? i + lag : nb));
+}
+
+// Page ids of a segment's blocks ahead of their use, 32 chunks to a warp's
+// register (a chunk is the part of a block that lies in one page).
+struct PageAhead {
+    int cur, next, group;
+};
+
+struct Barriers {
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t q_full;          // queries of a segment are in shared memory, the last outputs read
+    uint64_t s_full[2];       // a stream's scores are in tensor memory
+    uint64_t p_full[2];       // its weights are
+    uint64_t o_full[2];       // its last product is done
+    uint64_t drain;           // (after a wait ran out) the products in flight are done
+};
+
+struct Shared {
+    Barriers b;
+    Share share;
+    uint32_t tmem;
+    int gave_up;              // volatile use: a wait ran out somewhere
+    int strange;              // a value row of the segment's nodes is not finite
+    int last, more;
+    Segment seg;              // the softmax groups' segment, and where they are
+    SegmentWalk<kRows, kBlock, true> walk;
+    float m[kTile], l[kTile];
+};
+
+// Adds by hand what nodes with a non-finite value row (cleared for the products)
+// give to columns d0 .. d0 + 31 of a row: exact, and rare.
+template <int D>
+__device__ __forceinline__ void add_strange_nodes(const AttnParams &p, const Segment &seg, const __half *q,
+                                               const int32_t *tree_row, int node, float c, int d0, float (&o)[32])
+{
+    const int64_t ctx = seg.w.len - seg.w.nodes;
+    const int64_t lo = seg.b0 * kBlock, hi = (seg.b0 + seg.nb) * kBlock;
+    const int page = 1 << p.page_shift;
+    for (int64_t j = lo > ctx ? lo : ctx; j < hi && j < seg.w.len; ++j) {
+        if (!(seen_places(tree_row, p.tree_words, node, seg.w.nodes, seg.w.len, j) & 1u)) continue;
+        const int id = p.table[seg.r * p.width + (j >> p.page_shift)];
+        if (id < 0 || id >= p.n_pages) continue;
+        const int64_t row = id * p.page_stride +
+                            ((static_cast<int64_t>(seg.kvh) << p.page_shift) + (j & (page - 1))) * D;
+        const __half *v = static_cast<const __half *>(p.v) + row, *k = static_cast<const __half *>(p.k) + row;
+        bool odd = false;
+        for (int d = 0; d < D; ++d) odd |= (__half_as_ushort(v[d]) & 0x7c00u) == 0x7c00u;
+        if (!odd) continue;
+        float s = 0.0f;
+        for (int d = 0; d < D; ++d) s += __half2float(q[d]) * __half2float(k[d]);
+        const float w = exp2_fast(s * p.scale_log2 - c);
+#pragma unroll
+        for (int d = 0; d < 32; ++d) o[d] += w * __half2float(v[d0 + d]);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_tiles_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                           const AttnParams p)
+{
+    using R = Ring<D>;
+    using Walk = SegmentWalk<kRows, kBlock, true>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qbuf = smem;                          // two 128-row tiles of queries
+    uint8_t *ring = smem + 2 * R::kTileBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Barriers &b = sh.b;
+    volatile int *gave_up = &sh.gave_up;
+
+    if (tid == 0) {
+        for (int i = 0; i < R::kSlots; ++i) {
+            mbar_init(&b.kv_full[i], 1);
+            mbar_init(&b.kv_empty[i], 1);
+        }
+        mbar_init(&b.q_full, 8);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&b.s_full[x], 1);
+            mbar_init(&b.p_full[x], 4);
+            mbar_init(&b.o_full[x], 1);
+        }
+        mbar_init(&b.drain, 1);
+        sh.gave_up = 0;
+        sh.strange = 0;
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    pdl_allow_next_grid();
+    pdl_wait_prior_grid();
+    find_share<kRows, kBlock, true, kThreads>(p, &sh.share);   // ends with a block barrier
+    fence_after();
+    const uint32_t tmem = sh.tmem;
+    // Columns: scores of stream x (its weights over them) at 128 x, outputs at 256 + D x.
+
+    auto rows_of = [&](const Segment &s) -> int {
+        const int64_t left = static_cast<int64_t>(s.w.nodes) * p.group - static_cast<int64_t>(s.tile) * kRows;
+        return static_cast<int>(left < kRows ? left : kRows);
+    };
+
+    if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+        // ---------------- copies: one lane to each box ----------------
+        Walk walk;
+        Segment seg;
+        walk.begin(p, sh.share);
+        const int page = 1 << p.page_shift;
+        const int box_rows = page < kBlock ? page : kBlock;
+        const int chunks = kBlock / box_rows;      // of a block: 1 .. 8
+        uint32_t entry = 0;
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+            if (seg.w.bad) continue;               // its outputs are NaN, nothing is read
+            const int nb = static_cast<int>(seg.nb);
+            const int lag = rows_of(seg) > kTile ? 1 : 2;
+            const int64_t used = (seg.w.len + page - 1) >> p.page_shift;
+            const int32_t *trow = p.table + seg.r * p.width;
+            auto load_ids = [&](int group) -> int {
+                const int c = group * 32 + lane;
+                const int i = c / chunks;
+                const int64_t idx =
+                    ((seg.b0 + i) * kBlock + static_cast<int64_t>(c - i * chunks) * box_rows) >> p.page_shift;
+                if (i >= nb || idx >= used) return -1;
+                const int id = trow[idx];
+                return id < 0 || id >= p.n_pages ? 0 : id;   // a bad page: read another, the softmax side sees it too
+            };
+            PageAhead pk = {load_ids(0), load_ids(1), 0}, pv = pk;
+            auto ask = [&](int i, bool values) {
+                PageAhead &a = values ? pv : pk;
+                const int c0 = i * chunks;
+                if ((c0 >> 5) != a.group) {
+                    a.cur = a.next;
+                    a.group = c0 >> 5;
+                    a.next = load_ids(a.group + 1);
+                }
+                const uint32_t slot = entry % R::kSlots;
+                if (!warp_wait_or_give_up(&b.kv_empty[slot], ((entry / R::kSlots) & 1u) ^ 1u, gave_up, p.status)) {
+                    ok = false;
+                    return;
+                }
+                // lane l: half l / chunks of chunk l % chunks
+                const int c = lane % chunks, h = lane / chunks;
+                const int id = __shfl_sync(0xffffffffu, a.cur, (c0 + c) & 31);
+                const uint32_t there = __ballot_sync(0xffffffffu, h == 0 && id >= 0);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&b.kv_full[slot], __popc(there) * box_rows * 128 * R::kHalves);
+                __syncwarp();
+                if (h < R::kHalves && id >= 0) {
+                    const int64_t j = (seg.b0 + i) * kBlock + c * box_rows;
+                    copy_box(ring + slot * R::kTileBytes + h * R::kHalfBytes + c * box_rows * 128, values ? &vmap : &kmap,
+                             64 * h, (seg.kvh << p.page_shift) + (static_cast<int>(j & (page - 1)) & ~(box_rows - 1)), id,
+                             &b.kv_full[slot]);
+                }
+                __syncwarp();
+                ++entry;
+            };
+            for (int i = 0; ok && i < nb + lag; ++i) {
+                if (i >= lag) ask(i - lag, true);
+                if (ok && i < nb) ask(i, false);
+            }
+        }
+        if (!ok && lane == 0)   // copies in flight land before the CTA leaves
+            for (uint32_t n = entry > R::kSlots ? entry - R::kSlots : 0u; n < entry; ++n)
+                mbar_wait_bounded(&b.kv_full[n % R::kSlots], (n / R::kSlots) & 1u, nullptr);
+    } else if (warp == kMmaWarp) {
+        // ---------------- products: the warp runs the loop, one elected lane issues ----------------
+        constexpr uint32_t kScoreDesc = mma_desc(kBlock, false), kOutDesc = mma_desc(D, true);
+        const uint64_t qd = tile_desc(smem_u32(qbuf), 16), kd = tile_desc(smem_u32(ring), 16);
+        const uint64_t vd = tile_desc(smem_u32(ring), R::kHalfBytes);
+        Walk walk;
+        Segment seg;
+        walk.begin(p, sh.share);
+        uint32_t entry = 0, segs = 0, np[2] = {0, 0}, commits = 0;
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+            if (seg.w.bad) continue;   // nothing to multiply, its outputs are NaN
+            if (!warp_wait_or_give_up(&b.q_full, segs++ & 1u, gave_up, p.status)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            const int nb = static_cast<int>(seg.nb);
+            const bool two = rows_of(seg) > kTile;
+            const int lag = two ? 1 : 2;
+            auto wait_tile = [&](uint32_t n) {
+                const uint32_t e = entry + n;
+                ok = ok && warp_wait_or_give_up(&b.kv_full[e % R::kSlots], (e / R::kSlots) & 1u, gave_up, p.status);
+                return static_cast<uint64_t>((e % R::kSlots) * (R::kTileBytes >> 4));
+            };
+            for (int i = 0; ok && i < nb + lag; ++i) {
+                for (int x = two ? 0 : (i & 1); ok && x < (two ? 2 : (i & 1) + 1); ++x) {
+                    const bool last_use = !two || x == 1;
+                    if (i >= lag) {
+                        // o_x += p v of block i - lag
+                        const uint32_t sv = seq_v(i - lag, lag, nb);
+                        const uint64_t off = wait_tile(sv);
+                        ok = ok && warp_wait_or_give_up(&b.p_full[x], np[x]++ & 1u, gave_up, p.status);
+                        if (!ok) break;
+                        fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < kBlock / 16; ++ks)
+                                mma_ts(tmem + 256 + D * x, tmem + 128 * x + 8 * ks, vd + off + ks * (2048 >> 4), kOutDesc,
+                                       i - lag >= (two ? 1 : 2) || ks > 0);
+                            mma_commit(&b.o_full[x]);
+                            if (last_use) mma_commit(&b.kv_empty[(entry + sv) % R::kSlots]);
+                        }
+                        __syncwarp();
+                        ++commits;
+                    }
+                    if (i < nb) {
+                        // s_x = q_x k^T of block i, over the weights that the product just issued has read
+                        const uint32_t sk = seq_k(i, lag);
+                        const uint64_t off = wait_tile(sk);
+                        if (!ok) break;
+                        fence_after();
+                        if (elect_one()) {
+                            const uint64_t qx = qd + (two ? x : 0) * (R::kTileBytes >> 4);
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint32_t step = (ks >> 2) * (R::kHalfBytes >> 4) + (ks & 3) * 2;
+                                mma_ss(tmem + 128 * x, qx + step, kd + off + step, kScoreDesc, ks > 0);
+                            }
+                            mma_commit(&b.s_full[x]);
+                            if (last_use) mma_commit(&b.kv_empty[(entry + sk) % R::kSlots]);
+                        }
+                        __syncwarp();
+                        ++commits;
+                    }
+                }
+            }
+            entry += 2u * static_cast<uint32_t>(nb);
+        }
+        if (!ok && commits > 0) {   // products in flight end before the tensor memory is given back
+            if (elect_one()) mma_commit(&b.drain);
+            __syncwarp();
+            if (lane == 0) mbar_wait_bounded(&b.drain, 0, nullptr);
+            __syncwarp();
+        }
+    }
+    } else {
+        // ---------------- softmax: a thread to a row ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int x = warp >> 2;                   // stream
+        const int wt = tid & 127;                  // lane of tensor memory: row within the stream's tile
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t s_at = tmem + lanes + 128 * x, o_at = tmem + lanes + 256 + D * x;
+        // A negative scale turns the queries' signs; scale 0 clears them.
+        const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
+        const uint32_t q_and = p.scale_log2 == 0.0f ? 0u : 0xffffffffu, q_xor = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        uint32_t entry = 0, ns = 0, no = 0;        // ring entries, score tiles and outputs of this stream so far
+        bool ok = true;
+        // One thread walks; the segment lies in shared memory, out of the
+        // registers that the loop over the blocks needs.
+        const Segment &seg = sh.seg;
+        if (tid == 0) sh.walk.begin(p, sh.share);
+        while (true) {
+            if (tid == 0) sh.more = sh.walk.next(p, sh.seg) ? 1 : 0;
+            group_sync(1, 256);
+            if (!sh.more) break;
+            const int valid = rows_of(seg);
+            const bool two = valid > kTile;
+            const int lag = two ? 1 : 2;
+            const int nb = seg.w.bad ? 0 : static_cast<int>(seg.nb);
+            const int64_t len = seg.w.len, ctx = len - seg.w.nodes;
+            const int64_t first_token = p.start[seg.r] < 0 ? 0 : p.start[seg.r];
+            const int64_t row_base = static_cast<int64_t>(seg.tile) * kRows;
+            // ---- queries to shared memory; rows past the last one are zeros ----
+            bool bad = seg.w.bad;
+            if (!bad) {
+                const int n_rows = two ? kRows : kTile;
+                for (int i = tid; i < n_rows * (D / 8); i += 256) {
+                    const int row = i / (D / 8), c = i - row * (D / 8);
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < valid) {
+                        const int64_t rho = row_base + row, t = rho / p.group;
+                        v = *reinterpret_cast<const uint4 *>(p.q + (first_token + t) * p.q_stride +
+                                                             (seg.kvh * p.group + (rho - t * p.group)) * D + 8 * c);
+                        v.x = (v.x & q_and) ^ q_xor; v.y = (v.y & q_and) ^ q_xor;
+                        v.z = (v.z & q_and) ^ q_xor; v.w = (v.w & q_and) ^ q_xor;
+                    }
+                    const int r = row & 127;
+                    *reinterpret_cast<uint4 *>(qbuf + (row >> 7) * R::kTileBytes + (c >> 3) * R::kHalfBytes + r * 128 +
+                                               (((c & 7) ^ (r & 7)) << 4)) = v;
+                }
+                const int64_t used = (len + (1 << p.page_shift) - 1) >> p.page_shift;
+                const int64_t lo = (seg.b0 * kBlock) >> p.page_shift;
+                const int64_t hi = (((seg.b0 + nb) * kBlock - 1) >> p.page_shift) + 1;
+                for (int64_t i = lo + tid; i < hi && i < used; i += 256) {
+                    const int id = p.table[seg.r * p.width + i];
+                    bad |= id < 0 || id >= p.n_pages;
+                }
+            }
+            fence_async();
+            fence_before();
+            bad = group_or(1, 256, bad);
+            if (bad && tid == 0) atomicOr(p.status, kDevBadPage);
+            __syncwarp();
+            if (lane == 0 && !seg.w.bad) mbar_arrive(&b.q_full);
+
+            const int row = (two ? kTile * x : 0) + wt;              // row of the unit
+            const int64_t rho = row_base + row;
+            const int node = row < valid ? static_cast<int>(rho / p.group) : 0;
+            const int32_t *tree_row = p.tree ? p.tree + (first_token + node) * p.tree_words : nullptr;
+            // Places below `open` are seen by every row of this stream.
+            const int64_t open = p.tree ? ctx : ctx + (row_base + (two ? kTile * x : 0)) / p.group + 1;
+            float m = -INFINITY, l = 0.0f;
+            bool first = true;
+            for (int i = two ? 0 : x; i < nb; i += two ? 1 : 2) {
+                ok = ok && warp_wait_or_give_up(&b.s_full[x], ns++ & 1u, gave_up, p.status);
+                if (!ok) break;
+                fence_after();
+                const int64_t j0 = (seg.b0 + i) * kBlock;
+                const bool masked = j0 + kBlock > open;
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ld_32cols(s_at + 32 * c, s + 32 * c);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ld_wait(s + 32 * c);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t see = seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 32 * c);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u;   // -inf
+                    }
+                }
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 128; k += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        t[c] = fmaxf(t[c], fmaxf(__uint_as_float(s[k + 2 * c]), __uint_as_float(s[k + 2 * c + 1])));
+                const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+                const bool rises = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+                if (!first && __any_sync(0xffffffffu, rises)) {
+                    // the outputs so far follow the new maximum
+                    ok = ok && warp_wait_or_give_up(&b.o_full[x], (no - 1u) & 1u, gave_up, p.status);
+                    if (!ok) break;
+                    fence_after();
+                    const float f = rises ? exp2_fast(m - top) : 1.0f;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        ld_32cols(o_at + 32 * c, v);
+                        ld_wait(v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                        st_32cols(o_at + 32 * c, v);
+                    }
+                }
+                if (rises) m = top;
+                const float c0 = kShift - (m == -INFINITY ? 0.0f : m);
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float a = exp2_fast(fmaf(__uint_as_float(s[32 * c + 2 * k]), scale, c0));
+                        const float e = exp2_fast(fmaf(__uint_as_float(s[32 * c + 2 * k + 1]), scale, c0));
+                        sum[k & 3] += a + e;
+                        w[k] = float2_to_half2_bits(make_float2(a, e));
+                    }
+                    st_16cols(s_at + 16 * c, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (masked && j0 + wt >= ctx) {
+                    // Value rows past the end are cleared, and so are nodes' rows
+                    // that are not finite (add_strange_nodes adds those).
+                    const uint32_t e = entry + seq_v(i, lag, nb);
+                    ok = ok && wait_or_give_up(&b.kv_full[e % R::kSlots], (e / R::kSlots) & 1u, gave_up, p.status);
+                    uint8_t *v = ring + (e % R::kSlots) * R::kTileBytes + wt * 128;
+                    bool clear = j0 + wt >= len;
+                    if (ok && !clear) {
+#pragma unroll
+                        for (int h = 0; h < R::kHalves; ++h)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint4 q4 = *reinterpret_cast<const uint4 *>(v + h * R::kHalfBytes + ((c ^ (wt & 7)) << 4));
+                                const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    clear |= (u[k] & 0x7c00u) == 0x7c00u || (u[k] & 0x7c000000u) == 0x7c000000u;
+                            }
+                        if (clear) sh.strange = 1;
+                    }
+                    if (ok && clear)
+#pragma unroll
+                        for (int h = 0; h < R::kHalves; ++h)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                *reinterpret_cast<uint4 *>(v + h * R::kHalfBytes + (c << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_async();
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                st_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.p_full[x]);
+                ++no;
+                first = false;
+            }
+            entry += 2u * static_cast<uint32_t>(nb);
+            // ---- this stream's outputs are complete once its last product is ----
+            if (!first && ok) ok = warp_wait_or_give_up(&b.o_full[x], (no - 1u) & 1u, gave_up, p.status);
+            fence_after();
+            if (__any_sync(0xffffffffu, bad || !ok || *gave_up)) {
+                l = __int_as_float(0x7fffffff);
+                first = true;
+            }
+            group_sync(1, 256);                    // every value row has been looked at
+            const bool strange = sh.strange != 0;
+            float f = 1.0f;
+            if (!two) {
+                // Stream 1 hands its rows to stream 0 over the queries' shared memory.
+                float *xo = reinterpret_cast<float *>(qbuf);
+                if (x == 1) {
+                    sh.m[wt] = m;
+                    sh.l[wt] = l;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        if (!first) {
+                            ld_32cols(o_at + 32 * c, v);
+                            ld_wait(v);
+                        }
+                        if (wt < valid)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int at = ((c * 8 + k) + wt) & (D / 4 - 1);   // rows begin at different banks
+                                *reinterpret_cast<uint4 *>(xo + wt * D + 4 * at) =
+                                    first ? make_uint4(0u, 0u, 0u, 0u)
+                                          : make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                            }
+                    }
+                }
+                group_sync(1, 256);
+            }
+            const bool whole = seg.nb == seg.blocks;
+            float *part = whole ? nullptr : workspace_partial(p, blockIdx.x, seg.b0 == 0 ? 1 : 0, kRows, D);
+            if (two || x == 0) {
+                float f1 = 0.0f;
+                if (!two) {
+                    const float m1 = sh.m[wt], top = fmaxf(m, m1);
+                    f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+                    f1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
+                    const float l1 = sh.l[wt];
+                    l = (m == -INFINITY ? l : l * f) + (m1 == -INFINITY ? l1 : l1 * f1);
+                    m = top;
+                }
+                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+                const __half *q = nullptr;
+                if (strange && row < valid && !seg.w.bad)
+                    q = p.q + (first_token + node) * p.q_stride + (seg.kvh * p.group + (rho - static_cast<int64_t>(node) * p.group)) * D;
+                if (!whole && row < valid) {
+                    part[row] = m;
+                    part[kRows + row] = l;
+                }
+                __half *dst = whole && row < valid ? out_row<kRows, D>(p, seg, row) : nullptr;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    float o[32];
+                    __syncwarp();
+                    if (!first) {
+                        ld_32cols(o_at + 32 * c, v);
+                        ld_wait(v);
+                    }
+                    if (row >= valid) continue;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = first || f == 0.0f ? 0.0f : __uint_as_float(v[k]) * f;
+                    if (!two && f1 != 0.0f) {
+                        const float *xo = reinterpret_cast<const float *>(qbuf) + wt * D;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 a = *reinterpret_cast<const float4 *>(xo + 4 * (((c * 8 + k) + wt) & (D / 4 - 1)));
+                            o[4 * k] += a.x * f1; o[4 * k + 1] += a.y * f1;
+                            o[4 * k + 2] += a.z * f1; o[4 * k + 3] += a.w * f1;
+                        }
+                    }
+                    if (q) add_strange_nodes<D>(p, seg, q, tree_row, node, (m == -INFINITY ? 0.0f : m) - kShift, 32 * c, o);
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            float o8[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o8[i] = l == l ? o[k + i] * inv : l;
+                            store_half8(dst + 32 * c + k, o8);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(part + 2 * kRows + row * D + 32 * c + k) =
+                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                }
+            }
+            if (!whole) {
+                __threadfence();
+                group_sync(1, 256);
+                const int lead = owner_of(seg.unit_first, sh.share);
+                const int last = owner_of(seg.unit_first + seg.blocks - 1, sh.share);
+                if (tid == 0) {
+                    int *count = workspace_counters(p) + lead;
+                    const int seen = atomicAdd(count, 1);
+                    sh.last = seen == last - lead;
+                    if (sh.last) *count = 0;   // ready for the next call
+                }
+                group_sync(1, 256);
+                if (sh.last) {
+                    __threadfence();
+                    join_parts<kRows, D, 256>(p, seg, lead, last - lead + 1, valid, tid);
+                }
+            }
+            if (tid == 0) sh.strange = 0;
+            fence_before();
+            group_sync(1, 256);                    // the queries' memory may be written again
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int D>
+cudaError_t launch_with(const AttnParams &p, int sms, cudaStream_t s, bool pdl)
+{
+    const int page = 1 << p.page_shift;
+    const int rows = page < kBlock ? page : kBlock;
+    CUtensorMap kmap, vmap;
+    if (!encode_rows(&kmap, p, p.k, D, kKvF16, rows) || !encode_rows(&vmap, p, p.v, D, kKvF16, rows))
+        return cudaErrorInvalidValue;
+    auto kernel = tree_attn_tiles_kernel<D>;
+    cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(kernel), Ring<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    // The softmax groups' share of the registers exists only if the launch brings it.
+    static const int regs = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, tree_attn_tiles_kernel<D>) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    return launch_ex(kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads), Ring<D>::kSmem, s, pdl, kmap, vmap, p);
+}
+
+}  // namespace
+
+int64_t attn_tiles_workspace_floats(int sms) { return 2 * static_cast<int64_t>(sms) * partial_floats(kRows, 128); }
+
+cudaError_t launch_attn_tiles(const AttnParams &p, int D, int, int sms, cudaStream_t s, bool pdl)
+{
+    if (sms > kMaxGrid) return cudaErrorInvalidConfiguration;
+    return D == 64 ? launch_with<64>(p, sms, s, pdl) : launch_with<128>(p, sms, s, pdl);
+}
+
+}  // namespace qmv
