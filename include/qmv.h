@@ -439,9 +439,8 @@ QMV_API qmv_status qmv_kv_append(const void *qkv, int64_t stride, int qkv_f32, c
 
 /*
  * Bytes of workspace qmv_tree_attn takes on the current device, whatever the
- * sizes of the call (-1 on a CUDA error).  The caller zeroes it once; every
- * call leaves it ready for the next.  Calls that may run at the same time
- * need a workspace each.
+ * sizes of the call (-1 on a CUDA error).  Its contents need not be set or
+ * kept.  Calls that may run at the same time need a workspace each.
  */
 QMV_API int64_t qmv_tree_attn_workspace(void);
 

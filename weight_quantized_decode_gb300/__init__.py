@@ -199,9 +199,15 @@ def qmv_read_probe_ptr(buf: int, nbytes: int, out: int, stream: int = 0) -> None
 
 # -- torch-tensor entry points ---------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream):
@@ -524,23 +530,48 @@ class KvPages(NamedTuple):
     head: object       # [1] index in the free list after the last page taken
 
 
-def _int32(fn, name, t, dim):
-    torch = _torch()
-    if not t.is_cuda:
+# The paged-cache calls take a few microseconds on the GPU, so their checks look at each property of a tensor once
+# (get_device: the index, or -1 for a CPU tensor).
+
+def _on(fn, name, t, index):
+    got = t.get_device()
+    if got != index:
+        if got < 0 or index < 0:
+            raise TypeError(f"{fn}: {name} must be a CUDA tensor (no CPU path)")
+        raise ValueError(f"{fn}: all tensors must be on one device (cuda:{index} and {name} on cuda:{got})")
+
+
+def _int32(fn, name, t, dim, index):
+    if t.get_device() != index or index < 0:
+        _on(fn, name, t, index)
         raise TypeError(f"{fn}: {name} must be a CUDA tensor (no CPU path)")
-    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+    if t.dtype is not _torch().int32 or t.dim() != dim or not t.is_contiguous():
         raise TypeError(f"{fn}: {name} must be a contiguous int32 tensor with {dim} dimension" + ("s" if dim > 1 else ""))
     return t.data_ptr()
 
 
-def _tree_args(fn, tree, tokens):
+def _tree_args(fn, tree, tokens, index):
     """(address, words) of a tree mask [tokens, words], (0, 0) for none."""
     if tree is None:
         return 0, 0
-    ptr = _int32(fn, "tree", tree, 2)
+    ptr = _int32(fn, "tree", tree, 2, index)
     if tree.shape[0] != tokens or (tree.shape[1] == 0 and tokens > 0):
         raise ValueError(f"{fn}: tree must have a row of at least one word for each of the {tokens} tokens")
     return ptr, tree.shape[1]
+
+
+def _call_on(fn, index, stream, args):
+    """Calls library function `fn` with args and the stream's handle, device `index` current.  In the usual case (it
+    is current already and its current stream is meant) no Python object is made for either."""
+    torch = _torch()
+    f = getattr(_lib or lib(), fn)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            code = f(*args, _stream_handle(stream))
+    else:
+        code = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream))
+    if code != QMV_OK:
+        raise QmvError(fn, code)
 
 
 def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n_pages=None, stream=None):
@@ -550,28 +581,28 @@ def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n
     of the cache, to refuse wrong page ids (default: any that a slot can hold).  Returns KvPages."""
     torch = _torch()
     fn = "qmv_kv_pages"
-    a = [_int32(fn, "lens", lens, 1), _int32(fn, "n_new", n_new, 1), _int32(fn, "free", free, 1),
-         _int32(fn, "table", table, 2)]
+    at = lens.get_device()
+    len_ptr, new_ptr = _int32(fn, "lens", lens, 1, at), _int32(fn, "n_new", n_new, 1, at)
+    free_ptr, table_ptr = _int32(fn, "free", free, 1, at), _int32(fn, "table", table, 2, at)
     R, tokens, page = lens.shape[0], int(tokens), int(page)
     if n_new.shape[0] != R or table.shape[0] != R:
         raise ValueError(f"{fn}: lens, n_new and table must have one row to a request")
     if tokens < 0 or page <= 0:
         raise ValueError(f"{fn}: tokens must not be negative, page must be positive")
-    head_ptr = 0 if head is None else _int32(fn, "head", head, 1)
-    if head is not None and head.shape[0] != 1:
-        raise ValueError(f"{fn}: head must be one number")
-    tree_ptr, words = _tree_args(fn, tree, tokens)
-    others = [t for t in (n_new, free, table, head, tree) if t is not None]
-    with _on_device(fn, lens, *others):
-        out = torch.empty(2 * R + 2 + 3 * tokens, dtype=torch.int32, device=lens.device)
-        got = KvPages(*out.split((R + 1, R, tokens, tokens, tokens, 1)))
-        o, n = out.data_ptr(), 4 * tokens
-        s = o + 4 * (2 * R + 1)
-        _check(fn, lib().qmv_kv_pages(a[0], a[1], a[2], free.shape[0], head_ptr, tree_ptr, words, a[3], o,
-                                      o + 4 * (R + 1), s, s + n, s + 2 * n, s + 3 * n, R, table.shape[1], page,
-                                      (0x7fffffff // page) if n_pages is None else int(n_pages), tokens,
-                                      _stream_handle(stream)))
-    return got
+    head_ptr = 0
+    if head is not None:
+        head_ptr = _int32(fn, "head", head, 1, at)
+        if head.shape[0] != 1:
+            raise ValueError(f"{fn}: head must be one number")
+    tree_ptr, words = _tree_args(fn, tree, tokens, at)
+    out = torch.empty(2 * R + 2 + 3 * tokens, dtype=torch.int32, device=lens.device)
+    o, n = out.data_ptr(), 4 * tokens
+    s = o + 4 * (2 * R + 1)
+    _call_on(fn, at, stream,
+             (len_ptr, new_ptr, free_ptr, free.shape[0], head_ptr, tree_ptr, words, table_ptr, o, o + 4 * (R + 1), s,
+              s + n, s + 2 * n, s + 3 * n, R, table.shape[1], page,
+              (0x7fffffff // page) if n_pages is None else int(n_pages), tokens))
+    return KvPages(*out.split_with_sizes((R + 1, R, tokens, tokens, tokens, 1)))
 
 
 def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, interleaved=False, q=None, stream=None):
@@ -580,40 +611,40 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
     (None: not rotated); returns the rotated queries, fp16 [T, n_heads, D]."""
     torch = _torch()
     fn = "qmv_kv_append"
-    if not qkv.is_cuda:
-        raise TypeError(f"{fn}: qkv must be a CUDA tensor (no CPU path)")
-    if qkv.dtype not in (torch.float32, torch.float16):
+    at = qkv.get_device()
+    _on(fn, "cache", cache.k, at)
+    f32 = qkv.dtype is torch.float32
+    if not f32 and qkv.dtype is not torch.float16:
         raise TypeError(f"{fn}: qkv must be float32 or float16")
-    T, hk, D = qkv.shape[0], cache.kv_heads, cache.head_dim
-    if qkv.dim() != 2 or qkv.shape[1] != (n_heads + 2 * hk) * D or (T and qkv.stride(1) != 1):
+    hk, D = cache.kv_heads, cache.head_dim
+    if qkv.dim() != 2 or qkv.shape[1] != (n_heads + 2 * hk) * D or (qkv.shape[0] and qkv.stride(1) != 1):
         raise ValueError(f"{fn}: qkv must be [T, (n_heads + 2 * {hk}) * {D}] with dense rows")
-    slots_ptr = _int32(fn, "slots", slots, 1)
+    T, wide = qkv.shape
+    slots_ptr = _int32(fn, "slots", slots, 1, at)
     if slots.shape[0] != T:
         raise ValueError(f"{fn}: one slot to a token")
-    others = [slots, cache.k]
     pos_ptr = cos_ptr = sin_ptr = n_pos = rot = 0
     if (cos is None) != (sin is None) or (cos is not None and pos is None):
         raise ValueError(f"{fn}: a rotation takes pos, cos and sin")
     if cos is not None:
-        pos_ptr = _int32(fn, "pos", pos, 1)
+        pos_ptr = _int32(fn, "pos", pos, 1, at)
         if pos.shape[0] != T:
             raise ValueError(f"{fn}: one position to a token")
-        if not (cos.is_cuda and sin.is_cuda and cos.dtype == sin.dtype == torch.float32 and cos.dim() == 2
-                and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous()):
+        if not (cos.get_device() == sin.get_device() == at and cos.dtype is torch.float32 and sin.dtype is torch.float32
+                and cos.dim() == 2 and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous()):
             raise ValueError(f"{fn}: cos and sin must be contiguous CUDA float32 [positions, rot / 2]")
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        n_pos, rot = cos.shape
+        rot *= 2
         cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
-        others += [pos, cos, sin]
     if q is None:
         q = torch.empty((T, n_heads, D), dtype=torch.float16, device=qkv.device)
-    elif not (q.is_cuda and q.dtype == torch.float16 and q.is_contiguous() and q.numel() == T * n_heads * D):
+    elif not (q.get_device() == at and q.dtype is torch.float16 and q.is_contiguous() and q.numel() == T * n_heads * D):
         raise ValueError(f"{fn}: q must be a contiguous CUDA float16 tensor of {T}x{n_heads}x{D}")
     k, v, ks, vs, page_stride = cache._args
-    with _on_device(fn, qkv, q, *others):
-        _check(fn, lib().qmv_kv_append(qkv.data_ptr(), qkv.stride(0) if T > 1 else qkv.shape[1],
-                                       qkv.dtype == torch.float32, slots_ptr, pos_ptr, cos_ptr, sin_ptr, n_pos, rot,
-                                       bool(interleaved), q.data_ptr(), k, v, ks, vs, cache.kind, T, int(n_heads), hk,
-                                       D, cache.n_pages, cache.page, page_stride, _stream_handle(stream)))
+    _call_on(fn, at, stream,
+             (qkv.data_ptr(), qkv.stride(0) if T > 1 else wide, f32, slots_ptr, pos_ptr, cos_ptr, sin_ptr, n_pos, rot,
+              bool(interleaved), q.data_ptr(), k, v, ks, vs, cache.kind, T, int(n_heads), hk, D, cache.n_pages,
+              cache.page, page_stride))
     return q
 
 
@@ -626,7 +657,7 @@ def qmv_tree_attn_workspace(device=None):
         n = lib().qmv_tree_attn_workspace()
         if n < 0:
             raise QmvError("qmv_tree_attn_workspace", 6)
-        return torch.zeros(n, dtype=torch.uint8, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=None, workspace=None, stream=None):
@@ -636,35 +667,32 @@ def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=Non
     Returns fp16 [T, heads, D]."""
     torch = _torch()
     fn = "qmv_tree_attn"
-    if not q.is_cuda:
-        raise TypeError(f"{fn}: q must be a CUDA tensor (no CPU path)")
-    if q.dtype != torch.float16:
+    at = q.get_device()
+    _on(fn, "cache", cache.k, at)
+    if q.dtype is not torch.float16:
         raise TypeError(f"{fn}: q must be float16")
     D = cache.head_dim
     if q.dim() != 3 or q.shape[2] != D or (q.numel() and (q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != D))):
         raise ValueError(f"{fn}: q must be [T, heads, {D}] with dense rows")
-    T, H = q.shape[:2]
-    R = kv_len.shape[0]
-    a = [_int32(fn, "table", table, 2), _int32(fn, "start", start, 1), _int32(fn, "kv_len", kv_len, 1)]
-    if table.shape[0] != R or start.shape[0] != R + 1:
+    T, H, _ = q.shape
+    table_ptr, start_ptr, len_ptr = _int32(fn, "table", table, 2, at), _int32(fn, "start", start, 1, at), \
+        _int32(fn, "kv_len", kv_len, 1, at)
+    R, width = table.shape
+    if start.shape[0] != R + 1 or kv_len.shape[0] != R:
         raise ValueError(f"{fn}: table [R, width], start [R + 1] and kv_len [R] must agree")
-    tree_ptr, words = _tree_args(fn, tree, T)
+    tree_ptr, words = _tree_args(fn, tree, T, at)
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
-    elif not (out.is_cuda and out.dtype == torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
+    elif not (out.get_device() == at and out.dtype is torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
         raise ValueError(f"{fn}: out must be a contiguous CUDA float16 tensor of {T}x{H}x{D}")
     if workspace is None:
         workspace = qmv_tree_attn_workspace(q.device)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
+    elif not (workspace.get_device() == at and workspace.is_contiguous()):
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
-    others = [cache.k, table, start, kv_len, out, workspace] + ([tree] if tree is not None else [])
     k, v, ks, vs, page_stride = cache._args
-    with _on_device(fn, q, *others):
-        _check(fn, lib().qmv_tree_attn(q.data_ptr(), q.stride(0) if T > 1 else H * D, k, v, ks, vs, cache.kind,
-                                       cache.n_pages, cache.page, page_stride, a[0], table.shape[1], a[1], a[2],
-                                       tree_ptr, words,
-                                       None if scale is None else ctypes.byref(ctypes.c_float(scale)),
-                                       out.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), R, T, H, cache.kv_heads, D,
-                                       _stream_handle(stream)))
+    _call_on(fn, at, stream,
+             (q.data_ptr(), q.stride(0) if T > 1 else H * D, k, v, ks, vs, cache.kind, cache.n_pages, cache.page,
+              page_stride, table_ptr, width, start_ptr, len_ptr, tree_ptr, words,
+              None if scale is None else ctypes.byref(ctypes.c_float(scale)), out.data_ptr(), workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), R, T, H, cache.kv_heads, D))
     return out

@@ -51,15 +51,15 @@ bool encode_rows(CUtensorMap *map, const AttnParams &p, const void *base, int D,
 int64_t tree_attn_workspace_bytes(int sms)
 {
     const int64_t a = attn_rows_workspace_floats(sms), b = attn_tiles_workspace_floats(sms);
-    return 4 * (kMaxGrid + (a > b ? a : b));
+    return kUnitBytes + 4 * (a > b ? a : b);
 }
 
 cudaError_t launch_tree_attn(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl)
 {
-    // Rows that share a key/value head in the average request: up to 16 fill
-    // one tile of the streaming kernel; more go to the 128-row tiles.
+    // Rows that share a key/value head in the average request: up to 32 are
+    // one unit of the streaming kernel; more go to the 128-row tiles.
     const int64_t rows = (p.T + p.R - 1) / p.R * p.group;
-    if (rows <= 16 || kind == kKvQ8) return launch_attn_rows(p, D, kind, sms, s, pdl);
+    if (rows <= 32 || kind == kKvQ8) return launch_attn_rows(p, D, kind, rows, sms, s, pdl);
     return launch_attn_tiles(p, D, kind, sms, s, pdl);
 }
 

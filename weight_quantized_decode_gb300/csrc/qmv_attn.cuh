@@ -7,11 +7,13 @@
 // BLOCK.  All units' blocks, in order, are one long list, and CTA c of g takes
 // blocks [c B / g, (c + 1) B / g): the same share for each, however uneven the
 // requests are, with no plan made on the host.  A CTA's share is a run of
-// segments, each a range of one unit's blocks.  A unit that several CTAs share
-// is joined by the last of them to finish: each writes its rows' running
-// maximum, sum and unnormalised output (fp32) to its own place of the
-// workspace, and the last one adds them in CTA order, so that the result does
-// not depend on which one it was.
+// segments, each a range of one unit's blocks.  A CTA writes its part of a unit
+// that several CTAs share (its rows' running maximum, sum and unnormalised
+// output, fp32) to its own place of the workspace, and a second kernel adds a
+// unit's parts, in CTA order: the sum is the same on every run.  (Joined by the
+// last CTA to finish instead, 38 parts of 32 rows took 40 us, in two levels of
+// eight 14 us, each CTA reading alone; one tree of 8 nodes over 30001 places,
+// whose keys and values take 18 us.)
 #pragma once
 
 #include <cuda.h>
@@ -20,8 +22,17 @@
 
 #include "qmv_common.cuh"
 #include "qmv_kv.h"
+#include "qmv_launch.h"
 
 namespace qmv {
+
+// a / b for a, b >= 0, in 32 bits where they fit (a 64-bit division is a long
+// sequence of dependent instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 // Request r's share of the work.
 struct RequestWork {
@@ -41,7 +52,7 @@ __device__ __forceinline__ int64_t unit_blocks(const AttnParams &p, const Reques
     if (w.bad) return 1;
     int64_t places = w.len;
     if (CUT && !p.tree) {
-        const int64_t last = ((static_cast<int64_t>(tile) + 1) * ROWS - 1) / p.group;   // the tile's last token
+        const int64_t last = quotient((static_cast<int64_t>(tile) + 1) * ROWS - 1, p.group);   // the tile's last token
         if (last < w.nodes) places = w.len - w.nodes + last + 1;
     }
     return (places + BLOCK - 1) / BLOCK;
@@ -75,12 +86,13 @@ struct Share {
     int64_t total;       // all blocks
     int64_t r;           // the request block lo falls into
     int64_t before;      // blocks of the requests before it
+    RequestWork w;       // that request's work
     int g;               // CTAs that have a share
     int64_t sums[32];
-    int64_t found[2];
 };
 
 // Every thread of the block calls this (THREADS of them, a multiple of 32).
+// With up to THREADS requests each thread looks at one, once.
 template <int ROWS, int BLOCK, bool CUT, int THREADS>
 __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
 {
@@ -93,44 +105,53 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
             const int64_t u = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += u;
         }
-        __syncthreads();
         if (lane == 31) sh->sums[warp] = v;
         __syncthreads();
         int64_t add = 0, sum = 0;
+#pragma unroll
         for (int i = 0; i < W; ++i) {
             if (i < warp) add += sh->sums[i];
             sum += sh->sums[i];
         }
+        __syncthreads();
         *all = sum;
         return v + add;
     };
-    int64_t mine = 0, total = 0;
-    for (int64_t r = tid; r < p.R; r += THREADS) mine += request_work<ROWS, BLOCK, CUT>(p, r).total;
-    scan(mine, &total);
-    const int64_t g = total < gridDim.x ? total : static_cast<int64_t>(gridDim.x);
-    const int64_t lo = g > 0 && blockIdx.x < g ? total * blockIdx.x / g : 0;
-    const int64_t hi = g > 0 && blockIdx.x < g ? total * (blockIdx.x + 1) / g : 0;
-    int64_t before = 0;
-    for (int64_t r0 = 0; r0 < p.R && before <= lo && lo < hi; r0 += THREADS) {
-        const int64_t cnt = r0 + tid < p.R ? request_work<ROWS, BLOCK, CUT>(p, r0 + tid).total : 0;
-        int64_t all = 0;
-        const int64_t upto = before + scan(cnt, &all);
-        if (cnt > 0 && upto - cnt <= lo && lo < upto) {
-            sh->found[0] = r0 + tid;
-            sh->found[1] = upto - cnt;
-        }
-        before += all;
+    RequestWork w;
+    w.total = 0;
+    if (tid < p.R) w = request_work<ROWS, BLOCK, CUT>(p, tid);
+    int64_t total = 0;
+    int64_t upto = scan(w.total, &total);          // of the first THREADS requests
+    const int64_t chunk0 = total;
+    if (p.R > THREADS) {
+        int64_t more = 0, rest = 0;
+        for (int64_t r = THREADS + tid; r < p.R; r += THREADS) more += request_work<ROWS, BLOCK, CUT>(p, r).total;
+        scan(more, &rest);
+        total += rest;
     }
-    __syncthreads();
+    const int64_t g = total < gridDim.x ? total : static_cast<int64_t>(gridDim.x);
+    const bool mine = blockIdx.x < g;
+    const int64_t lo = mine ? quotient(total * blockIdx.x, g) : 0, hi = mine ? quotient(total * (blockIdx.x + 1), g) : 0;
     if (tid == 0) {
         sh->lo = lo;
         sh->hi = hi;
         sh->total = total;
         sh->g = static_cast<int>(g);
-        if (lo < hi) {
-            sh->r = sh->found[0];
-            sh->before = sh->found[1];
+    }
+    int64_t before = chunk0;
+    for (int64_t r = tid;;) {
+        if (w.total > 0 && upto - w.total <= lo && lo < upto && mine) {
+            sh->r = r;
+            sh->before = upto - w.total;
+            sh->w = w;
         }
+        r += THREADS;
+        if (r - tid >= p.R || before > lo || !mine) break;
+        w.total = 0;
+        if (r < p.R) w = request_work<ROWS, BLOCK, CUT>(p, r);
+        int64_t all = 0;
+        upto = before + scan(w.total, &all);
+        before += all;
     }
     __syncthreads();
 }
@@ -157,13 +178,13 @@ struct SegmentWalk {
         hi = sh.hi;
         if (at >= hi) return;
         u.r = sh.r;
-        u.w = request_work<ROWS, BLOCK, CUT>(p, u.r);
-        u.kvh = static_cast<int>((at - sh.before) / u.w.per_head);
+        u.w = sh.w;
+        u.kvh = static_cast<int>(quotient(at - sh.before, u.w.per_head));
         u.unit_first = sh.before + u.kvh * u.w.per_head;
         u.tile = 0;
         u.blocks = unit_blocks<ROWS, BLOCK, CUT>(p, u.w, 0);
         if (!CUT) {   // units of one size
-            u.tile = static_cast<int>((at - u.unit_first) / u.blocks);
+            u.tile = static_cast<int>(quotient(at - u.unit_first, u.blocks));
             u.unit_first += u.tile * u.blocks;
         }
         while (at >= u.unit_first + u.blocks) step(p);
@@ -197,7 +218,7 @@ struct SegmentWalk {
 // The CTA whose share holds block b of the list.
 __device__ __forceinline__ int owner_of(int64_t b, const Share &sh)
 {
-    return static_cast<int>(((b + 1) * sh.g - 1) / sh.total);
+    return static_cast<int>(quotient((b + 1) * sh.g - 1, sh.total));
 }
 
 // Which of the 32 places j0 .. j0 + 31 a row's token sees, as bits.  node: its
@@ -263,28 +284,39 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// Workspace: a counter to each CTA of the grid, then for each CTA two places
-// for partial results (a unit it finishes for others, and one it begins).
-// A place: m[ROWS], l[ROWS], o[ROWS][D], fp32.
-constexpr int kMaxGrid = 4096;
+// Workspace: what each CTA of the grid leaves to join, then for each CTA two
+// places for partial results (a unit it ends or passes on, and one it begins).
+// A place: m[ROWS], l[ROWS], o[D / 4][ROWS][4], fp32 (neighbouring threads hold
+// neighbouring rows or neighbouring columns: either way they write whole lines).
+constexpr int kMaxGrid = 1024;
+
+// The shared unit that a CTA begins (parts 0: none).
+struct alignas(32) SharedUnit {
+    int parts;          // CTAs that share it, this one first
+    int valid;          // its rows
+    int kvh, tile;
+    int64_t first_row;  // its request's first token
+    int64_t pad;
+};
+constexpr int64_t kUnitBytes = kMaxGrid * sizeof(SharedUnit);
+
 __host__ __device__ constexpr int64_t partial_floats(int rows, int D) { return static_cast<int64_t>(rows) * (D + 2); }
 
-__device__ __forceinline__ int *workspace_counters(const AttnParams &p) { return static_cast<int *>(p.workspace); }
+__device__ __forceinline__ SharedUnit *workspace_units(const AttnParams &p) { return static_cast<SharedUnit *>(p.workspace); }
 __device__ __forceinline__ float *workspace_partial(const AttnParams &p, int cta, int which, int rows, int D)
 {
-    return reinterpret_cast<float *>(static_cast<int *>(p.workspace) + kMaxGrid) +
+    return reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kUnitBytes) +
            (2 * static_cast<int64_t>(cta) + which) * partial_floats(rows, D);
 }
 
-// The output row of row `row` of a segment's unit.
+// The output row of row `row` of a unit.
 template <int ROWS, int D>
-__device__ __forceinline__ __half *out_row(const AttnParams &p, const Segment &s, int row)
+__device__ __forceinline__ __half *out_row(const AttnParams &p, int64_t first_token, int kvh, int tile, int row)
 {
-    const int64_t rho = static_cast<int64_t>(s.tile) * ROWS + row;
-    const int64_t token = rho / p.group;
-    const int head = s.kvh * p.group + static_cast<int>(rho - token * p.group);
-    const int64_t first = p.start[s.r] < 0 ? 0 : p.start[s.r];
-    return p.out + ((first + token) * p.Hq + head) * D;
+    const uint32_t rho = static_cast<uint32_t>(tile) * ROWS + row;   // T * Hq fits 32 bits
+    const uint32_t token = rho / static_cast<uint32_t>(p.group);
+    const int head = kvh * p.group + static_cast<int>(rho - token * p.group);
+    return p.out + ((first_token + token) * p.Hq + head) * D;
 }
 
 __device__ __forceinline__ void store_half8(__half *dst, const float (&v)[8])
@@ -297,38 +329,146 @@ __device__ __forceinline__ void store_half8(__half *dst, const float (&v)[8])
     *reinterpret_cast<uint4 *>(dst) = w;
 }
 
-// Joins a unit of `rows` valid rows whose parts are in the workspace: called by
-// the THREADS threads (tid 0 ..) of the CTA that finished last, which has seen
-// the others' parts published.  Part i lies with CTA first + i; the first one
-// in its second place, the others in their first.
-template <int ROWS, int D, int THREADS>
-__device__ __forceinline__ void join_parts(const AttnParams &p, const Segment &s, int first, int parts, int rows, int tid)
+// Columns d .. d + 3 of row `row` in such a place.
+template <int ROWS>
+__device__ __forceinline__ float4 *part_columns(float *part, int row, int d)
 {
-    constexpr int CH = D / 8;   // 8 values to a thread at a time
-    for (int i = tid; i < rows * CH; i += THREADS) {
-        const int row = i / CH, d = (i - row * CH) * 8;
-        float m = -INFINITY;
-        for (int c = 0; c < parts; ++c)
-            m = fmaxf(m, __ldcg(workspace_partial(p, first + c, c == 0, ROWS, D) + row));
-        const float mm = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, o[8] = {};
-#pragma unroll 4
-        for (int c = 0; c < parts; ++c) {
-            const float *part = workspace_partial(p, first + c, c == 0, ROWS, D);
-            const float f = exp2_fast(__ldcg(part + row) - mm);
-            l += __ldcg(part + ROWS + row) * f;
-            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part + 2 * ROWS + row * D + d));
-            const float4 b = __ldcg(reinterpret_cast<const float4 *>(part + 2 * ROWS + row * D + d + 4));
-            if (f > 0.0f) {   // a part whose rows saw nothing adds nothing
-                o[0] += a.x * f; o[1] += a.y * f; o[2] += a.z * f; o[3] += a.w * f;
-                o[4] += b.x * f; o[5] += b.y * f; o[6] += b.z * f; o[7] += b.w * f;
+    return reinterpret_cast<float4 *>(part + 2 * ROWS) + (d >> 2) * ROWS + row;
+}
+
+// Leaves word of the shared unit that segment s begins.
+__device__ __forceinline__ void leave_unit(const AttnParams &p, const Segment &s, const Share &sh, int valid, int64_t first_token)
+{
+    SharedUnit u;
+    u.parts = owner_of(s.unit_first + s.blocks - 1, sh) - static_cast<int>(blockIdx.x) + 1;
+    u.valid = valid;
+    u.kvh = s.kvh;
+    u.tile = s.tile;
+    u.first_row = first_token;
+    u.pad = 0;
+    workspace_units(p)[blockIdx.x] = u;
+}
+
+// ---- the second kernel: adds the parts of shared units ----
+//
+// Block x looks at what CTAS CTAs of the first kernel left; block y takes every
+// gridDim.y-th run of a unit's pieces (8 columns of a row each, rows next to
+// each other).  A unit of up to four parts: each thread adds a piece.  More:
+// the four warps take every fourth part of the same 32 pieces, and their sums
+// are added in shared memory.  Eight parts' loads are in flight at a time.
+constexpr int kJoinThreads = 128;
+
+template <int ROWS, int D, int CTAS>
+__global__ void __launch_bounds__(kJoinThreads) join_units_kernel(const AttnParams p, int grid)
+{
+    constexpr int CH = D / 8;
+    constexpr int kAhead = 8;
+    __shared__ float sums[4][32][12];
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c0 = blockIdx.x * CTAS;
+    const int mine = lane < CTAS && c0 + lane < grid ? __ldcg(&workspace_units(p)[c0 + lane].parts) : 0;
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine > 1); left; left &= left - 1u) {
+        const int cta = c0 + __ffs(left) - 1;
+        const SharedUnit u = workspace_units(p)[cta];
+        const int pieces = u.valid * CH;
+        const bool split = u.parts > 4;                  // a piece's parts over the warps
+        const int run = split ? 32 : kJoinThreads, stride = split ? 4 : 1;
+        for (int base = run * blockIdx.y; base < pieces; base += run * gridDim.y) {
+            const int at = base + (split ? lane : static_cast<int>(threadIdx.x));
+            const bool on = at < pieces;
+            const int piece = on ? at : pieces - 1;
+            const int chunk = piece / u.valid, row = piece - chunk * u.valid, d = 8 * chunk;
+            float m = -INFINITY, l = 0.0f, o[8] = {};
+            for (int k0 = split ? warp : 0; k0 < u.parts; k0 += stride * kAhead) {
+                float mc[kAhead], lc[kAhead];
+                float4 a[kAhead], b[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    mc[k] = -INFINITY;
+                    lc[k] = 0.0f;
+                    a[k] = b[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    const int part_no = k0 + stride * k;
+                    if (part_no < u.parts) {
+                        float *part = workspace_partial(p, cta + part_no, part_no == 0, ROWS, D);
+                        mc[k] = __ldcg(part + row);
+                        lc[k] = __ldcg(part + ROWS + row);
+                        a[k] = __ldcg(part_columns<ROWS>(part, row, d));
+                        b[k] = __ldcg(part_columns<ROWS>(part, row, d + 4));
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) top = fmaxf(top, mc[k]);
+                const float tt = top == -INFINITY ? 0.0f : top;
+                const float f0 = exp2_fast(m - tt);
+                l *= f0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] *= f0;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float f = exp2_fast(mc[k] - tt);
+                    // a part whose rows saw nothing adds nothing (but a NaN sum says
+                    // that the request cannot be read)
+                    l += lc[k] != lc[k] ? lc[k] : lc[k] * f;
+                    if (f > 0.0f) {
+                        o[0] += a[k].x * f; o[1] += a[k].y * f; o[2] += a[k].z * f; o[3] += a[k].w * f;
+                        o[4] += b[k].x * f; o[5] += b[k].y * f; o[6] += b[k].z * f; o[7] += b[k].w * f;
+                    }
+                }
+                m = top;
+            }
+            if (split) {
+                float *mine4 = sums[warp][lane];
+                *reinterpret_cast<float2 *>(mine4) = make_float2(m, l);
+                *reinterpret_cast<float4 *>(mine4 + 4) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<float4 *>(mine4 + 8) = make_float4(o[4], o[5], o[6], o[7]);
+                __syncthreads();
+                if (warp == 0) {
+                    float top = m;
+#pragma unroll
+                    for (int w = 1; w < 4; ++w) top = fmaxf(top, sums[w][lane][0]);
+                    const float tt = top == -INFINITY ? 0.0f : top;
+                    l = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float *x = sums[w][lane];
+                        const float f = exp2_fast(x[0] - tt);
+                        l += x[1] != x[1] ? x[1] : x[1] * f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] += f > 0.0f ? x[4 + j] * f : 0.0f;
+                    }
+                }
+                __syncthreads();
+            }
+            if (on && (!split || warp == 0)) {
+                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = l == l ? o[j] * inv : l;
+                store_half8(out_row<ROWS, D>(p, u.first_row, u.kvh, u.tile, row) + d, o);
             }
         }
-        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = l == l ? o[k] * inv : l;
-        store_half8(out_row<ROWS, D>(p, s, row) + d, o);
     }
+}
+
+// Launches it behind a kernel of `grid` CTAs, unless no unit can have had more
+// than one block.
+template <int ROWS, int D>
+cudaError_t launch_join(const AttnParams &p, int grid, int block, cudaStream_t s, bool pdl)
+{
+    if ((p.width << p.page_shift) <= block) return cudaSuccess;
+    // 32 rows: 16 runs of pieces; 256 rows: a block to each CTA, 16 runs of 256
+    constexpr int kCtas = ROWS > 64 ? 1 : 8, kRuns = ROWS * D / 8 / 32 < 16 ? ROWS * D / 8 / 32 : 16;
+    return launch_ex(join_units_kernel<ROWS, D, kCtas>, dim3((grid + kCtas - 1) / kCtas, kRuns), dim3(kJoinThreads), 0, s, pdl,
+                     p, grid);
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // Tensor copy of one box of cached rows: x the first column, y the row within
@@ -348,7 +488,8 @@ bool encode_rows(CUtensorMap *map, const AttnParams &p, const void *base, int D,
 
 // The two kernels' launches (qmv_attn_rows.cu, qmv_attn_tiles.cu) and the
 // workspace each needs.
-cudaError_t launch_attn_rows(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl);
+// rows: query rows that share a key/value head in the average request.
+cudaError_t launch_attn_rows(const AttnParams &p, int D, int kind, int64_t rows, int sms, cudaStream_t s, bool pdl);
 cudaError_t launch_attn_tiles(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl);
 int64_t attn_rows_workspace_floats(int sms);
 int64_t attn_tiles_workspace_floats(int sms);

@@ -96,16 +96,6 @@ __device__ __forceinline__ void st_32cols(uint32_t taddr, const uint32_t *v)
         : "memory");
 }
 
-__device__ __forceinline__ void st_16cols(uint32_t taddr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptors, 128-byte swizzle.  Rows of 128 bytes, eight
@@ -149,6 +139,28 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar)
                  : "memory");
 }
 
+// Two fp32 values to a 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Barrier `id` among `n` threads; the OR of their flags.
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ bool group_or(int id, int n, bool flag)
@@ -181,10 +193,25 @@ struct PageAhead {
 struct Barriers {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t q_full;          // queries of a segment are in shared memory, the last outputs read
-    uint64_t s_full[2];       // a stream's scores are in tensor memory
-    uint64_t p_full[2];       // its weights are
-    uint64_t o_full[2];       // its last product is done
+    uint64_t s_full[2];       // a stream's scores of a block are in tensor memory
+    uint64_t p_full[2][2];    // a half of its weights is
+    uint64_t o_full[2][2];    // that half's product with values is done
     uint64_t drain;           // (after a wait ran out) the products in flight are done
+};
+
+// Where a role is: one of its threads walks, and the segment lies in shared
+// memory, out of the registers that the loops over the blocks need.
+struct Where {
+    Segment seg;
+    SegmentWalk<kRows, kBlock, true> walk;
+    int more;
+    __device__ __forceinline__ bool next_for_warp(const AttnParams &p)
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) more = walk.next(p, seg) ? 1 : 0;
+        __syncwarp();
+        return more != 0;
+    }
 };
 
 struct Shared {
@@ -193,9 +220,7 @@ struct Shared {
     uint32_t tmem;
     int gave_up;              // volatile use: a wait ran out somewhere
     int strange;              // a value row of the segment's nodes is not finite
-    int last, more;
-    Segment seg;              // the softmax groups' segment, and where they are
-    SegmentWalk<kRows, kBlock, true> walk;
+    Where where[3];           // the softmax groups, the copies, the products
     float m[kTile], l[kTile];
 };
 
@@ -232,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const AttnParams p)
 {
     using R = Ring<D>;
-    using Walk = SegmentWalk<kRows, kBlock, true>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Shared sh;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -243,6 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *gave_up = &sh.gave_up;
 
     if (tid == 0) {
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
         for (int i = 0; i < R::kSlots; ++i) {
             mbar_init(&b.kv_full[i], 1);
             mbar_init(&b.kv_empty[i], 1);
@@ -250,8 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&b.q_full, 8);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&b.s_full[x], 1);
-            mbar_init(&b.p_full[x], 4);
-            mbar_init(&b.o_full[x], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&b.p_full[x][h], 4);
+                mbar_init(&b.o_full[x][h], 1);
+            }
         }
         mbar_init(&b.drain, 1);
         sh.gave_up = 0;
@@ -264,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     fence_before();
-    pdl_allow_next_grid();
     pdl_wait_prior_grid();
     find_share<kRows, kBlock, true, kThreads>(p, &sh.share);   // ends with a block barrier
     fence_after();
@@ -280,17 +307,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
         // ---------------- copies: one lane to each box ----------------
-        Walk walk;
-        Segment seg;
-        walk.begin(p, sh.share);
+        Where &at = sh.where[1];
+        const Segment &seg = at.seg;
+        if (lane == 0) at.walk.begin(p, sh.share);
         const int page = 1 << p.page_shift;
         const int box_rows = page < kBlock ? page : kBlock;
         const int chunks = kBlock / box_rows;      // of a block: 1 .. 8
         uint32_t entry = 0;
         bool ok = true;
-        while (ok && walk.next(p, seg)) {
+        while (ok && at.next_for_warp(p)) {
             if (seg.w.bad) continue;               // its outputs are NaN, nothing is read
             const int nb = static_cast<int>(seg.nb);
+            const int64_t b0 = seg.b0;
+            const int y_head = seg.kvh << p.page_shift;
             const int lag = rows_of(seg) > kTile ? 1 : 2;
             const int64_t used = (seg.w.len + page - 1) >> p.page_shift;
             const int32_t *trow = p.table + seg.r * p.width;
@@ -298,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c = group * 32 + lane;
                 const int i = c / chunks;
                 const int64_t idx =
-                    ((seg.b0 + i) * kBlock + static_cast<int64_t>(c - i * chunks) * box_rows) >> p.page_shift;
+                    ((b0 + i) * kBlock + static_cast<int64_t>(c - i * chunks) * box_rows) >> p.page_shift;
                 if (i >= nb || idx >= used) return -1;
                 const int id = trow[idx];
                 return id < 0 || id >= p.n_pages ? 0 : id;   // a bad page: read another, the softmax side sees it too
@@ -325,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&b.kv_full[slot], __popc(there) * box_rows * 128 * R::kHalves);
                 __syncwarp();
                 if (h < R::kHalves && id >= 0) {
-                    const int64_t j = (seg.b0 + i) * kBlock + c * box_rows;
+                    const int64_t j = (b0 + i) * kBlock + c * box_rows;
                     copy_box(ring + slot * R::kTileBytes + h * R::kHalfBytes + c * box_rows * 128, values ? &vmap : &kmap,
-                             64 * h, (seg.kvh << p.page_shift) + (static_cast<int>(j & (page - 1)) & ~(box_rows - 1)), id,
+                             64 * h, y_head + (static_cast<int>(j & (page - 1)) & ~(box_rows - 1)), id,
                              &b.kv_full[slot]);
                 }
                 __syncwarp();
@@ -346,12 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kScoreDesc = mma_desc(kBlock, false), kOutDesc = mma_desc(D, true);
         const uint64_t qd = tile_desc(smem_u32(qbuf), 16), kd = tile_desc(smem_u32(ring), 16);
         const uint64_t vd = tile_desc(smem_u32(ring), R::kHalfBytes);
-        Walk walk;
-        Segment seg;
-        walk.begin(p, sh.share);
-        uint32_t entry = 0, segs = 0, np[2] = {0, 0}, commits = 0;
+        Where &at = sh.where[2];
+        const Segment &seg = at.seg;
+        if (lane == 0) at.walk.begin(p, sh.share);
+        uint32_t entry = 0, segs = 0, np = 0, commits = 0;   // np: the phases of p_full, a bit to a stream
         bool ok = true;
-        while (ok && walk.next(p, seg)) {
+        while (ok && at.next_for_warp(p)) {
             if (seg.w.bad) continue;   // nothing to multiply, its outputs are NaN
             if (!warp_wait_or_give_up(&b.q_full, segs++ & 1u, gave_up, p.status)) {
                 ok = false;
@@ -367,29 +396,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return static_cast<uint64_t>((e % R::kSlots) * (R::kTileBytes >> 4));
             };
             for (int i = 0; ok && i < nb + lag; ++i) {
+                const uint32_t sv = i >= lag ? seq_v(i - lag, lag, nb) : 0u, sk = seq_k(i, lag);
                 for (int x = two ? 0 : (i & 1); ok && x < (two ? 2 : (i & 1) + 1); ++x) {
                     const bool last_use = !two || x == 1;
                     if (i >= lag) {
-                        // o_x += p v of block i - lag
-                        const uint32_t sv = seq_v(i - lag, lag, nb);
+                        // o_x += p v of block i - lag, each half as its weights arrive
                         const uint64_t off = wait_tile(sv);
-                        ok = ok && warp_wait_or_give_up(&b.p_full[x], np[x]++ & 1u, gave_up, p.status);
-                        if (!ok) break;
-                        fence_after();
-                        if (elect_one()) {
 #pragma unroll
-                            for (int ks = 0; ks < kBlock / 16; ++ks)
-                                mma_ts(tmem + 256 + D * x, tmem + 128 * x + 8 * ks, vd + off + ks * (2048 >> 4), kOutDesc,
-                                       i - lag >= (two ? 1 : 2) || ks > 0);
-                            mma_commit(&b.o_full[x]);
-                            if (last_use) mma_commit(&b.kv_empty[(entry + sv) % R::kSlots]);
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && warp_wait_or_give_up(&b.p_full[x][h], (np >> x) & 1u, gave_up, p.status);
+                            if (!ok) break;
+                            fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                                    mma_ts(tmem + 256 + D * x, tmem + 128 * x + 64 * h + 8 * (ks - 4 * h),
+                                           vd + off + ks * (2048 >> 4), kOutDesc, i >= 2 * lag || ks > 0);
+                                mma_commit(&b.o_full[x][h]);
+                                if (h == 1 && last_use) mma_commit(&b.kv_empty[(entry + sv) % R::kSlots]);
+                            }
+                            __syncwarp();
+                            ++commits;
                         }
-                        __syncwarp();
-                        ++commits;
+                        np ^= 1u << x;
+                        if (!ok) break;
                     }
                     if (i < nb) {
-                        // s_x = q_x k^T of block i, over the weights that the product just issued has read
-                        const uint32_t sk = seq_k(i, lag);
+                        // s_x = q_x k^T of block i, over the weights that the products just
+                        // issued read first (the products of a CTA run in the order of issue)
                         const uint64_t off = wait_tile(sk);
                         if (!ok) break;
                         fence_after();
@@ -427,40 +461,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A negative scale turns the queries' signs; scale 0 clears them.
         const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
         const uint32_t q_and = p.scale_log2 == 0.0f ? 0u : 0xffffffffu, q_xor = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-        uint32_t entry = 0, ns = 0, no = 0;        // ring entries, score tiles and outputs of this stream so far
+        uint32_t entry = 0, ns = 0;                // ring entries so far; phase of this stream's blocks
         bool ok = true;
-        // One thread walks; the segment lies in shared memory, out of the
-        // registers that the loop over the blocks needs.
-        const Segment &seg = sh.seg;
-        if (tid == 0) sh.walk.begin(p, sh.share);
+        Where &at = sh.where[0];
+        const Segment &seg = at.seg;
+        bool left_unit = false;                    // word of a shared unit left for the second kernel
+        if (tid == 0) at.walk.begin(p, sh.share);
         while (true) {
-            if (tid == 0) sh.more = sh.walk.next(p, sh.seg) ? 1 : 0;
+            if (tid == 0) at.more = at.walk.next(p, at.seg) ? 1 : 0;
             group_sync(1, 256);
-            if (!sh.more) break;
+            if (!at.more) break;
             const int valid = rows_of(seg);
             const bool two = valid > kTile;
             const int lag = two ? 1 : 2;
             const int nb = seg.w.bad ? 0 : static_cast<int>(seg.nb);
-            const int64_t len = seg.w.len, ctx = len - seg.w.nodes;
+            const int64_t len = seg.w.len, ctx = len - seg.w.nodes, b0 = seg.b0;
             const int64_t first_token = p.start[seg.r] < 0 ? 0 : p.start[seg.r];
             const int64_t row_base = static_cast<int64_t>(seg.tile) * kRows;
             // ---- queries to shared memory; rows past the last one are zeros ----
             bool bad = seg.w.bad;
             if (!bad) {
-                const int n_rows = two ? kRows : kTile;
-                for (int i = tid; i < n_rows * (D / 8); i += 256) {
-                    const int row = i / (D / 8), c = i - row * (D / 8);
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < valid) {
-                        const int64_t rho = row_base + row, t = rho / p.group;
-                        v = *reinterpret_cast<const uint4 *>(p.q + (first_token + t) * p.q_stride +
-                                                             (seg.kvh * p.group + (rho - t * p.group)) * D + 8 * c);
-                        v.x = (v.x & q_and) ^ q_xor; v.y = (v.y & q_and) ^ q_xor;
-                        v.z = (v.z & q_and) ^ q_xor; v.w = (v.w & q_and) ^ q_xor;
+                // a thread's 16-byte chunk is the same in each of its rows; eight loads in flight
+                constexpr int kStride = 256 / (D / 8);
+                const int c = tid & (D / 8 - 1);
+                for (int r0 = tid / (D / 8); r0 < (two ? kRows : kTile); r0 += 8 * kStride) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = r0 + k * kStride;
+                        v[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < valid) {
+                            const uint32_t rho = static_cast<uint32_t>(row_base) + r, t = rho / static_cast<uint32_t>(p.group);
+                            v[k] = *reinterpret_cast<const uint4 *>(
+                                p.q + (first_token + t) * p.q_stride + (seg.kvh * p.group + (rho - t * p.group)) * D + 8 * c);
+                        }
                     }
-                    const int r = row & 127;
-                    *reinterpret_cast<uint4 *>(qbuf + (row >> 7) * R::kTileBytes + (c >> 3) * R::kHalfBytes + r * 128 +
-                                               (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = (r0 + k * kStride) & 127;
+                        const uint4 u = make_uint4((v[k].x & q_and) ^ q_xor, (v[k].y & q_and) ^ q_xor,
+                                                   (v[k].z & q_and) ^ q_xor, (v[k].w & q_and) ^ q_xor);
+                        *reinterpret_cast<uint4 *>(qbuf + ((r0 + k * kStride) >> 7) * R::kTileBytes + (c >> 3) * R::kHalfBytes +
+                                                   r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
+                    }
                 }
                 const int64_t used = (len + (1 << p.page_shift) - 1) >> p.page_shift;
                 const int64_t lo = (seg.b0 * kBlock) >> p.page_shift;
@@ -479,113 +522,125 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             const int row = (two ? kTile * x : 0) + wt;              // row of the unit
             const int64_t rho = row_base + row;
-            const int node = row < valid ? static_cast<int>(rho / p.group) : 0;
+            const int node = row < valid ? static_cast<int>(static_cast<uint32_t>(rho) / static_cast<uint32_t>(p.group)) : 0;
             const int32_t *tree_row = p.tree ? p.tree + (first_token + node) * p.tree_words : nullptr;
             // Places below `open` are seen by every row of this stream.
-            const int64_t open = p.tree ? ctx : ctx + (row_base + (two ? kTile * x : 0)) / p.group + 1;
+            const int64_t open =
+                p.tree ? ctx : ctx + static_cast<uint32_t>(row_base + (two ? kTile * x : 0)) / static_cast<uint32_t>(p.group) + 1;
             float m = -INFINITY, l = 0.0f;
             bool first = true;
-            for (int i = two ? 0 : x; i < nb; i += two ? 1 : 2) {
-                ok = ok && warp_wait_or_give_up(&b.s_full[x], ns++ & 1u, gave_up, p.status);
+            for (int i = two ? 0 : x; ok && i < nb; i += two ? 1 : 2, ns ^= 1u) {
+                const int64_t j0 = (b0 + i) * kBlock;
+                const bool masked = j0 + kBlock > open;
+                ok = warp_wait_or_give_up(&b.s_full[x], ns, gave_up, p.status);
                 if (!ok) break;
                 fence_after();
-                const int64_t j0 = (seg.b0 + i) * kBlock;
-                const bool masked = j0 + kBlock > open;
-                uint32_t s[128];
+                // The scores were issued after every earlier product of the stream:
+                // its outputs are at rest until this block's first weights are given.
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t s[64];
+                    ld_32cols(s_at + 64 * h, s);
+                    ld_32cols(s_at + 64 * h + 32, s + 32);
+                    ld_wait(s);
+                    ld_wait(s + 32);
+                    if (masked) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) ld_32cols(s_at + 32 * c, s + 32 * c);
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t see =
+                                seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 64 * h + 32 * c);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) ld_wait(s + 32 * c);
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t see = seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 32 * c);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u;   // -inf
+                            for (int k = 0; k < 32; ++k)
+                                if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u;   // -inf
+                        }
                     }
-                }
-                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t w[32];
+                    uint64_t sum[2];
+                    // Weights by the maximum so far, beside the maximum of these
+                    // scores; where one lies past the lag, the outputs follow the new
+                    // maximum and the weights are taken again.
+                    while (true) {
+                        const float c0 = kShift - (m == -INFINITY ? 0.0f : m);
+                        const uint64_t scale2 = pair(scale, scale), c2 = pair(c0, c0);
+                        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        sum[0] = sum[1] = 0ull;
 #pragma unroll
-                for (int k = 0; k < 128; k += 8)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        t[c] = fmaxf(t[c], fmaxf(__uint_as_float(s[k + 2 * c]), __uint_as_float(s[k + 2 * c + 1])));
-                const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
-                const bool rises = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
-                if (!first && __any_sync(0xffffffffu, rises)) {
-                    // the outputs so far follow the new maximum
-                    ok = ok && warp_wait_or_give_up(&b.o_full[x], (no - 1u) & 1u, gave_up, p.status);
-                    if (!ok) break;
-                    fence_after();
-                    const float f = rises ? exp2_fast(m - top) : 1.0f;
-                    l *= f;
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        ld_32cols(o_at + 32 * c, v);
-                        ld_wait(v);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                        st_32cols(o_at + 32 * c, v);
-                    }
-                }
-                if (rises) m = top;
-                const float c0 = kShift - (m == -INFINITY ? 0.0f : m);
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float a = exp2_fast(fmaf(__uint_as_float(s[32 * c + 2 * k]), scale, c0));
-                        const float e = exp2_fast(fmaf(__uint_as_float(s[32 * c + 2 * k + 1]), scale, c0));
-                        sum[k & 3] += a + e;
-                        w[k] = float2_to_half2_bits(make_float2(a, e));
-                    }
-                    st_16cols(s_at + 16 * c, w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if (masked && j0 + wt >= ctx) {
-                    // Value rows past the end are cleared, and so are nodes' rows
-                    // that are not finite (add_strange_nodes adds those).
-                    const uint32_t e = entry + seq_v(i, lag, nb);
-                    ok = ok && wait_or_give_up(&b.kv_full[e % R::kSlots], (e / R::kSlots) & 1u, gave_up, p.status);
-                    uint8_t *v = ring + (e % R::kSlots) * R::kTileBytes + wt * 128;
-                    bool clear = j0 + wt >= len;
-                    if (ok && !clear) {
-#pragma unroll
-                        for (int h = 0; h < R::kHalves; ++h)
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const uint4 q4 = *reinterpret_cast<const uint4 *>(v + h * R::kHalfBytes + ((c ^ (wt & 7)) << 4));
-                                const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    clear |= (u[k] & 0x7c00u) == 0x7c00u || (u[k] & 0x7c000000u) == 0x7c000000u;
+                        for (int k = 0; k < 32; ++k) {
+                            const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
+                            const uint64_t e = fma2(pair(s0, s1), scale2, c2);
+                            const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
+                            sum[k & 1] = add2(sum[k & 1], pair(a, c));
+                            w[k] = float2_to_half2_bits(make_float2(a, c));
+                            t[k & 3] = fmaxf(t[k & 3], fmaxf(s0, s1));
+                        }
+                        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+                        const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
+                        if (!__any_sync(0xffffffffu, rises)) break;
+                        if (!first) {
+                            if (h == 1) {
+                                ok = warp_wait_or_give_up(&b.o_full[x][0], ns, gave_up, p.status);
+                                if (!ok) break;
+                                fence_after();
                             }
-                        if (clear) sh.strange = 1;
+                            const float f = rises ? exp2_fast(m - top) : 1.0f;
+                            l *= f;
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t v[32];
+                                ld_32cols(o_at + 32 * c, v);
+                                ld_wait(v);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                                st_32cols(o_at + 32 * c, v);
+                            }
+                        }
+                        if (rises) m = top;
                     }
-                    if (ok && clear)
+                    if (!ok) break;
+                    st_32cols(s_at + 64 * h, w);
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += low(sum[0]) + high(sum[0]);
+                    if (masked && (wt >> 6) == h && j0 + wt >= ctx) {
+                        // Value rows past the end are cleared, and so are nodes' rows
+                        // that are not finite (add_strange_nodes adds those).
+                        const uint32_t e = entry + seq_v(i, lag, nb);
+                        ok = ok && wait_or_give_up(&b.kv_full[e % R::kSlots], (e / R::kSlots) & 1u, gave_up, p.status);
+                        uint8_t *v = ring + (e % R::kSlots) * R::kTileBytes + wt * 128;
+                        bool clear = j0 + wt >= len;
+                        if (ok && !clear) {
 #pragma unroll
-                        for (int h = 0; h < R::kHalves; ++h)
+                            for (int hh = 0; hh < R::kHalves; ++hh)
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                *reinterpret_cast<uint4 *>(v + h * R::kHalfBytes + (c << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_async();
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 q4 =
+                                        *reinterpret_cast<const uint4 *>(v + hh * R::kHalfBytes + ((c ^ (wt & 7)) << 4));
+                                    const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        clear |= (u[k] & 0x7c00u) == 0x7c00u || (u[k] & 0x7c000000u) == 0x7c000000u;
+                                }
+                            if (clear) sh.strange = 1;
+                        }
+                        if (ok && clear)
+#pragma unroll
+                            for (int hh = 0; hh < R::kHalves; ++hh)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(v + hh * R::kHalfBytes + (c << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_async();
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.p_full[x][h]);
+                    first = false;
                 }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                st_wait();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p_full[x]);
-                ++no;
-                first = false;
             }
             entry += 2u * static_cast<uint32_t>(nb);
             // ---- this stream's outputs are complete once its last product is ----
-            if (!first && ok) ok = warp_wait_or_give_up(&b.o_full[x], (no - 1u) & 1u, gave_up, p.status);
+            if (!first && ok) ok = warp_wait_or_give_up(&b.o_full[x][1], ns ^ 1u, gave_up, p.status);
             fence_after();
             if (__any_sync(0xffffffffu, bad || !ok || *gave_up)) {
                 l = __int_as_float(0x7fffffff);
@@ -639,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[row] = m;
                     part[kRows + row] = l;
                 }
-                __half *dst = whole && row < valid ? out_row<kRows, D>(p, seg, row) : nullptr;
+                __half *dst = whole && row < valid ? out_row<kRows, D>(p, first_token, seg.kvh, seg.tile, row) : nullptr;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
@@ -673,34 +728,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(part + 2 * kRows + row * D + 32 * c + k) =
-                                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                            *part_columns<kRows>(part, row, 32 * c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                     }
                 }
             }
-            if (!whole) {
-                __threadfence();
-                group_sync(1, 256);
-                const int lead = owner_of(seg.unit_first, sh.share);
-                const int last = owner_of(seg.unit_first + seg.blocks - 1, sh.share);
-                if (tid == 0) {
-                    int *count = workspace_counters(p) + lead;
-                    const int seen = atomicAdd(count, 1);
-                    sh.last = seen == last - lead;
-                    if (sh.last) *count = 0;   // ready for the next call
-                }
-                group_sync(1, 256);
-                if (sh.last) {
-                    __threadfence();
-                    join_parts<kRows, D, 256>(p, seg, lead, last - lead + 1, valid, tid);
-                }
+            if (tid == 0 && !whole && seg.b0 == 0) {
+                left_unit = true;
+                leave_unit(p, seg, sh.share, valid, first_token);
             }
             if (tid == 0) sh.strange = 0;
             fence_before();
             group_sync(1, 256);                    // the queries' memory may be written again
         }
+        if (tid == 0 && !left_unit) workspace_units(p)[blockIdx.x].parts = 0;
     }
     fence_before();
+    pdl_allow_next_grid();
     __syncthreads();
     if (warp == kMmaWarp) {
         fence_after();
@@ -725,7 +768,9 @@ cudaError_t launch_with(const AttnParams &p, int sms, cudaStream_t s, bool pdl)
         return cudaFuncGetAttributes(&a, tree_attn_tiles_kernel<D>) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    return launch_ex(kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads), Ring<D>::kSmem, s, pdl, kmap, vmap, p);
+    e = launch_ex(kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads), Ring<D>::kSmem, s, pdl, kmap, vmap, p);
+    if (e != cudaSuccess) return e;
+    return launch_join<kRows, D>(p, sms, kBlock, s, pdl);
 }
 
 }  // namespace
