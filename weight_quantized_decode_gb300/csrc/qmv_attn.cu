@@ -59,7 +59,7 @@ cudaError_t launch_tree_attn(const AttnParams &p, int D, int kind, int sms, cuda
     // Rows that share a key/value head in the average request: up to 32 are
     // one unit of the streaming kernel; more go to the 128-row tiles.
     const int64_t rows = (p.T + p.R - 1) / p.R * p.group;
-    if (rows <= 32 || kind == kKvQ8) return launch_attn_rows(p, D, kind, rows, sms, s, pdl);
+    if (rows <= 32) return launch_attn_rows(p, D, kind, rows, sms, s, pdl);
     return launch_attn_tiles(p, D, kind, sms, s, pdl);
 }
 

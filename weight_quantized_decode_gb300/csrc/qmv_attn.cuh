@@ -5,8 +5,10 @@
 // A unit is one (request, key/value head, tile of ROWS query rows); a row is
 // one (new token, query head of the group).  Its places are cut into blocks of
 // BLOCK.  All units' blocks, in order, are one long list, and CTA c of g takes
-// blocks [c B / g, (c + 1) B / g): the same share for each, however uneven the
-// requests are, with no plan made on the host.  A CTA's share is a run of
+// entries [c B / g, (c + 1) B / g): the same share for each, however uneven the
+// requests are, with no plan made on the host.  A unit begins with COST entries
+// that stand for no block but for what a CTA spends on a unit besides its
+// blocks (queries, start and end of the pipeline).  A CTA's share is a run of
 // segments, each a range of one unit's blocks.  A CTA writes its part of a unit
 // that several CTAs share (its rows' running maximum, sum and unnormalised
 // output, fp32) to its own place of the workspace, and a second kernel adds a
@@ -40,25 +42,25 @@ struct RequestWork {
     int tiles;         // row tiles
     int64_t len;       // places
     bool bad;          // a length the cache cannot have: one block that gives NaN
-    int64_t per_head;  // blocks of the units of one key/value head
-    int64_t total;     // blocks of all its units
+    int64_t per_head;  // entries of the units of one key/value head
+    int64_t total;     // entries of all its units
 };
 
-// Blocks of the unit of row tile `tile`.  CUT: the rows of a chain see nothing
+// Entries of the unit of row tile `tile`: COST and its blocks.  CUT: the rows of a chain see nothing
 // past the tile's last token, and the blocks there are left out.
-template <int ROWS, int BLOCK, bool CUT>
-__device__ __forceinline__ int64_t unit_blocks(const AttnParams &p, const RequestWork &w, int tile)
+template <int ROWS, int BLOCK, int COST, bool CUT>
+__device__ __forceinline__ int64_t unit_entries(const AttnParams &p, const RequestWork &w, int tile)
 {
-    if (w.bad) return 1;
+    if (w.bad) return COST + 1;
     int64_t places = w.len;
     if (CUT && !p.tree) {
         const int64_t last = quotient((static_cast<int64_t>(tile) + 1) * ROWS - 1, p.group);   // the tile's last token
         if (last < w.nodes) places = w.len - w.nodes + last + 1;
     }
-    return (places + BLOCK - 1) / BLOCK;
+    return COST + (places + BLOCK - 1) / BLOCK;
 }
 
-template <int ROWS, int BLOCK, bool CUT>
+template <int ROWS, int BLOCK, int COST, bool CUT>
 __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t r)
 {
     RequestWork w;
@@ -72,9 +74,9 @@ __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t
     w.tiles = static_cast<int>((static_cast<int64_t>(w.nodes) * p.group + ROWS - 1) / ROWS);
     if (CUT && !p.tree) {
         w.per_head = 0;
-        for (int t = 0; t < w.tiles; ++t) w.per_head += unit_blocks<ROWS, BLOCK, CUT>(p, w, t);
+        for (int t = 0; t < w.tiles; ++t) w.per_head += unit_entries<ROWS, BLOCK, COST, CUT>(p, w, t);
     } else {
-        w.per_head = w.tiles * unit_blocks<ROWS, BLOCK, CUT>(p, w, 0);
+        w.per_head = w.tiles * unit_entries<ROWS, BLOCK, COST, CUT>(p, w, 0);
     }
     w.total = w.per_head * p.Hkv;
     return w;
@@ -82,10 +84,10 @@ __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t
 
 // Where a CTA's share begins, in shared memory (find_share).
 struct Share {
-    int64_t lo, hi;      // blocks [lo, hi) of the list
-    int64_t total;       // all blocks
-    int64_t r;           // the request block lo falls into
-    int64_t before;      // blocks of the requests before it
+    int64_t lo, hi;      // entries [lo, hi) of the list
+    int64_t total;       // all entries
+    int64_t r;           // the request entry lo falls into
+    int64_t before;      // entries of the requests before it
     RequestWork w;       // that request's work
     int g;               // CTAs that have a share
     int64_t sums[32];
@@ -93,7 +95,7 @@ struct Share {
 
 // Every thread of the block calls this (THREADS of them, a multiple of 32).
 // With up to THREADS requests each thread looks at one, once.
-template <int ROWS, int BLOCK, bool CUT, int THREADS>
+template <int ROWS, int BLOCK, int COST, bool CUT, int THREADS>
 __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
 {
     constexpr int W = THREADS / 32;
@@ -119,13 +121,13 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
     };
     RequestWork w;
     w.total = 0;
-    if (tid < p.R) w = request_work<ROWS, BLOCK, CUT>(p, tid);
+    if (tid < p.R) w = request_work<ROWS, BLOCK, COST, CUT>(p, tid);
     int64_t total = 0;
     int64_t upto = scan(w.total, &total);          // of the first THREADS requests
     const int64_t chunk0 = total;
     if (p.R > THREADS) {
         int64_t more = 0, rest = 0;
-        for (int64_t r = THREADS + tid; r < p.R; r += THREADS) more += request_work<ROWS, BLOCK, CUT>(p, r).total;
+        for (int64_t r = THREADS + tid; r < p.R; r += THREADS) more += request_work<ROWS, BLOCK, COST, CUT>(p, r).total;
         scan(more, &rest);
         total += rest;
     }
@@ -148,7 +150,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
         r += THREADS;
         if (r - tid >= p.R || before > lo || !mine) break;
         w.total = 0;
-        if (r < p.R) w = request_work<ROWS, BLOCK, CUT>(p, r);
+        if (r < p.R) w = request_work<ROWS, BLOCK, COST, CUT>(p, r);
         int64_t all = 0;
         upto = before + scan(w.total, &all);
         before += all;
@@ -156,70 +158,83 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
     __syncthreads();
 }
 
+// The CTA of g whose share holds entry e of the list's `total`.
+__device__ __forceinline__ int owner_of(int64_t e, int g, int64_t total)
+{
+    return static_cast<int>(quotient((e + 1) * g - 1, total));
+}
+
 // A CTA's part of one unit.
 struct Segment {
     int64_t r;            // request
     int kvh, tile;        // key/value head, row tile
     int64_t b0, nb;       // its blocks [b0, b0 + nb) of the unit
-    int64_t blocks;       // blocks of the unit
-    int64_t unit_first;   // the list's index of the unit's first block
+    bool whole;           // they are all
+    int parts;            // CTAs that share the unit, if this one begins it; else 0
+    int64_t entries;      // entries of the unit
+    int64_t unit_first;   // the list's index of the first of them
     RequestWork w;
 };
 
 // Walks a CTA's segments (begin, then next until it is false).  Any number of
 // threads may each keep one.
-template <int ROWS, int BLOCK, bool CUT>
+template <int ROWS, int BLOCK, int COST, bool CUT>
 struct SegmentWalk {
-    int64_t at, hi;
-    Segment u;            // the unit that `at` falls into (b0, nb unused)
+    int64_t at, hi, total;
+    int g;
+    Segment u;            // the unit that `at` falls into
     __device__ __forceinline__ void begin(const AttnParams &p, const Share &sh)
     {
         at = sh.lo;
         hi = sh.hi;
+        total = sh.total;
+        g = sh.g;
         if (at >= hi) return;
         u.r = sh.r;
         u.w = sh.w;
         u.kvh = static_cast<int>(quotient(at - sh.before, u.w.per_head));
         u.unit_first = sh.before + u.kvh * u.w.per_head;
         u.tile = 0;
-        u.blocks = unit_blocks<ROWS, BLOCK, CUT>(p, u.w, 0);
+        u.entries = unit_entries<ROWS, BLOCK, COST, CUT>(p, u.w, 0);
         if (!CUT) {   // units of one size
-            u.tile = static_cast<int>(quotient(at - u.unit_first, u.blocks));
-            u.unit_first += u.tile * u.blocks;
+            u.tile = static_cast<int>(quotient(at - u.unit_first, u.entries));
+            u.unit_first += u.tile * u.entries;
         }
-        while (at >= u.unit_first + u.blocks) step(p);
+        while (at >= u.unit_first + u.entries) step(p);
     }
     // To the unit that follows.
     __device__ __forceinline__ void step(const AttnParams &p)
     {
-        u.unit_first += u.blocks;
+        u.unit_first += u.entries;
         if (++u.tile == u.w.tiles) {
             u.tile = 0;
             if (++u.kvh == p.Hkv) {
                 u.kvh = 0;
-                do u.w = request_work<ROWS, BLOCK, CUT>(p, ++u.r);
+                do u.w = request_work<ROWS, BLOCK, COST, CUT>(p, ++u.r);
                 while (u.w.total == 0);
             }
         }
-        u.blocks = unit_blocks<ROWS, BLOCK, CUT>(p, u.w, u.tile);
+        u.entries = unit_entries<ROWS, BLOCK, COST, CUT>(p, u.w, u.tile);
     }
     __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
     {
-        if (at >= hi) return false;
-        if (at >= u.unit_first + u.blocks) step(p);
-        s = u;
-        s.b0 = at - u.unit_first;
-        s.nb = u.blocks - s.b0 < hi - at ? u.blocks - s.b0 : hi - at;
-        at += s.nb;
-        return true;
+        while (at < hi) {
+            if (at >= u.unit_first + u.entries) step(p);
+            const int64_t unit_end = u.unit_first + u.entries, end = unit_end < hi ? unit_end : hi;
+            const int64_t from = at - u.unit_first - COST, to = end - u.unit_first - COST;
+            at = end;
+            if (to <= 0) continue;   // none of its blocks
+            s = u;
+            s.b0 = from > 0 ? from : 0;
+            s.nb = to - s.b0;
+            s.whole = s.nb == u.entries - COST;
+            s.parts = 0;
+            if (!s.whole && s.b0 == 0) s.parts = owner_of(unit_end - 1, g, total) - static_cast<int>(blockIdx.x) + 1;
+            return true;
+        }
+        return false;
     }
 };
-
-// The CTA whose share holds block b of the list.
-__device__ __forceinline__ int owner_of(int64_t b, const Share &sh)
-{
-    return static_cast<int>(quotient((b + 1) * sh.g - 1, sh.total));
-}
 
 // Which of the 32 places j0 .. j0 + 31 a row's token sees, as bits.  node: its
 // index among the request's `nodes` new tokens; tree_row its mask, or NULL.
@@ -337,10 +352,10 @@ __device__ __forceinline__ float4 *part_columns(float *part, int row, int d)
 }
 
 // Leaves word of the shared unit that segment s begins.
-__device__ __forceinline__ void leave_unit(const AttnParams &p, const Segment &s, const Share &sh, int valid, int64_t first_token)
+__device__ __forceinline__ void leave_unit(const AttnParams &p, const Segment &s, int valid, int64_t first_token)
 {
     SharedUnit u;
-    u.parts = owner_of(s.unit_first + s.blocks - 1, sh) - static_cast<int>(blockIdx.x) + 1;
+    u.parts = s.parts;
     u.valid = valid;
     u.kvh = s.kvh;
     u.tile = s.tile;

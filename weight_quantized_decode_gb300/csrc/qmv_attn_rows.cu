@@ -31,6 +31,7 @@ namespace {
 constexpr int kBlock = 128;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCost = 2;            // what a unit costs besides its blocks, in blocks
 constexpr int kStep = 32;           // places of a warp's step
 constexpr float kShift = 10.0f;     // weights are 2^10 times exp(s - max)
 
@@ -148,9 +149,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
         mbar_init_fence();
     }
     pdl_wait_prior_grid();
-    find_share<kRows, kBlock, false, kThreads>(p, &sh);
+    find_share<kRows, kBlock, kCost, false, kThreads>(p, &sh);
 
-    SegmentWalk<kRows, kBlock, false> walk;
+    SegmentWalk<kRows, kBlock, kCost, false> walk;
     walk.begin(p, sh);
     Segment seg;
     // The ring: the slot that is consumed next and its phase; requests refill
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
                 }
             }
         __syncthreads();
-        const bool whole = seg.nb == seg.blocks;
+        const bool whole = seg.whole;
         const int64_t first_out = first_token < 0 ? 0 : first_token;
         float *part = whole ? nullptr : workspace_partial(p, blockIdx.x, seg.b0 == 0 ? 1 : 0, kRows, D);
         for (int i = tid; i < valid * (D / 8); i += kThreads) {
@@ -693,9 +694,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
                 *part_columns<kRows>(part, row, d + 4) = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
-        if (!whole && seg.b0 == 0) {
+        if (seg.parts > 0) {
             left_unit = true;
-            if (tid == 0) leave_unit(p, seg, sh, valid, first_out);
+            if (tid == 0) leave_unit(p, seg, valid, first_out);
         }
         __syncthreads();    // the scratch is the ring again
     }

@@ -32,22 +32,38 @@ namespace {
 constexpr int kTile = 128;           // rows of a stream
 constexpr int kRows = 2 * kTile;     // rows of a unit
 constexpr int kBlock = 128;          // places of a block
+constexpr int kCost = 6;             // what a unit costs besides its blocks, in blocks
 constexpr int kMmaWarp = 8, kCopyWarp = 9;
-constexpr int kThreads = 384;        // three warpgroups; warps 10 and 11 have nothing to do
-// Registers of a thread: at launch, and after the softmax groups have taken
-// what the others give up (the shares add up to the launch's).
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 224, kOtherRegs = 56;
-static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "shares of the launch's registers");
+constexpr int kExpandWarp = 12;      // 12-15, for 8-bit rows only
 constexpr float kShift = 10.0f;      // weights are 2^10 times exp(s - max)
 constexpr float kLazy = 5.0f;        // a maximum may lag this far (log2)
 
-template <int D>
+template <int D, int KIND>
 struct Ring {
     static constexpr int kHalves = D / 64;                      // 64-column halves of a tile
     static constexpr int kHalfBytes = kBlock * 128;
     static constexpr int kTileBytes = kHalves * kHalfBytes;     // 128 rows of fp16
-    static constexpr int kSlots = D == 128 ? 4 : 8;             // 128 KB of keys and values
-    static constexpr size_t kSmem = 1024 + static_cast<size_t>(2 + kSlots) * kTileBytes;
+    // fp16: 128 KB of keys and values.  8-bit rows: 96 KB of expanded tiles, the
+    // copies' own ring of codes (a tile, and with keys the block's two vectors of
+    // scales), and the blocks' scales as the softmax reads them.
+    static constexpr int kSlots = (KIND == kKvF16 ? 131072 : 98304) / kTileBytes;
+    static constexpr int kCodeBytes = kBlock * D;
+    static constexpr int kRawBytes = kCodeBytes + 2 * kBlock * 4;
+    static constexpr int kRaw = KIND == kKvF16 ? 1 : kSlots;
+    // Blocks whose scales are kept: those that the copies and the expanding warps
+    // may be ahead, two tiles to a block, and the two in work.
+    static constexpr int kScales = KIND == kKvF16 ? 1 : (D == 128 ? 8 : 16);
+    static constexpr int kRawAt = (2 + kSlots) * kTileBytes;
+    static constexpr int kScaleAt = kRawAt + kRaw * kRawBytes;
+    static constexpr size_t kSmem = 1024 + (KIND == kKvF16 ? kRawAt : kScaleAt + kScales * 2 * kBlock * 4);
+    // Registers of a thread: at launch, and after the softmax groups have taken
+    // what the others give up (the shares add up to the launch's).
+    static constexpr int kThreads = KIND == kKvF16 ? 384 : 512;
+    static constexpr int kLaunchRegs = KIND == kKvF16 ? 168 : 128;
+    static constexpr int kSoftmaxRegs = KIND == kKvF16 ? 224 : 176, kOtherRegs = KIND == kKvF16 ? 56 : 64;
+    static constexpr int kExpandRegs = 96;
+    static_assert(2 * kSoftmaxRegs + kOtherRegs + (KIND == kKvF16 ? 0 : kExpandRegs) == kThreads / 128 * kLaunchRegs,
+                  "shares of the launch's registers");
 };
 
 // ---- tensor memory and products -----------------------------------------------
@@ -146,12 +162,19 @@ __device__ __forceinline__ uint64_t pair(float a, float b)
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }   // -126 .. 127
 __device__ __forceinline__ float low(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float high(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
@@ -192,6 +215,8 @@ struct PageAhead {
 
 struct Barriers {
     uint64_t kv_full[8], kv_empty[8];
+    uint64_t raw_full[8], raw_empty[8];   // 8-bit rows: the copies' ring of codes
+    uint64_t scale_full[16];              // and the blocks' scales
     uint64_t q_full;          // queries of a segment are in shared memory, the last outputs read
     uint64_t s_full[2];       // a stream's scores of a block are in tensor memory
     uint64_t p_full[2][2];    // a half of its weights is
@@ -203,7 +228,7 @@ struct Barriers {
 // memory, out of the registers that the loops over the blocks need.
 struct Where {
     Segment seg;
-    SegmentWalk<kRows, kBlock, true> walk;
+    SegmentWalk<kRows, kBlock, kCost, true> walk;
     int more;
     __device__ __forceinline__ bool next_for_warp(const AttnParams &p)
     {
@@ -220,8 +245,13 @@ struct Shared {
     uint32_t tmem;
     int gave_up;              // volatile use: a wait ran out somewhere
     int strange;              // a value row of the segment's nodes is not finite
-    Where where[3];           // the softmax groups, the copies, the products
+    Where where[4];           // the softmax groups, the copies, the products, the expanding warps
     float m[kTile], l[kTile];
+    int ve;
+    // 8-bit rows, of each block kept: by 32 places, which value scales are not
+    // finite, and the exponent above the largest of the others
+    uint32_t odd[16][4];
+    int exponent[16][4];
 };
 
 // Adds by hand what nodes with a non-finite value row (cleared for the products)
@@ -251,12 +281,12 @@ __device__ __forceinline__ void add_strange_nodes(const AttnParams &p, const Seg
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int KIND>
+__global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
     tree_attn_tiles_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const AttnParams p)
 {
-    using R = Ring<D>;
+    using R = Ring<D, KIND>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ Shared sh;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -270,9 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_map(&kmap);
         prefetch_map(&vmap);
         for (int i = 0; i < R::kSlots; ++i) {
-            mbar_init(&b.kv_full[i], 1);
+            mbar_init(&b.kv_full[i], KIND == kKvF16 ? 1 : 4);
             mbar_init(&b.kv_empty[i], 1);
         }
+        for (int i = 0; KIND == kKvQ8 && i < R::kRaw; ++i) {
+            mbar_init(&b.raw_full[i], 1);
+            mbar_init(&b.raw_empty[i], 4);
+        }
+        for (int i = 0; KIND == kKvQ8 && i < R::kScales; ++i) mbar_init(&b.scale_full[i], 4);
         mbar_init(&b.q_full, 8);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&b.s_full[x], 1);
@@ -293,9 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before();
     pdl_wait_prior_grid();
-    find_share<kRows, kBlock, true, kThreads>(p, &sh.share);   // ends with a block barrier
+    find_share<kRows, kBlock, kCost, true, R::kThreads>(p, &sh.share);   // ends with a block barrier
     fence_after();
     const uint32_t tmem = sh.tmem;
+    constexpr uint32_t kCopyRing = KIND == kKvF16 ? R::kSlots : R::kRaw;
     // Columns: scores of stream x (its weights over them) at 128 x, outputs at 256 + D x.
 
     auto rows_of = [&](const Segment &s) -> int {
@@ -303,8 +339,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         return static_cast<int>(left < kRows ? left : kRows);
     };
 
-    if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (KIND == kKvQ8 && warp >= kExpandWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kExpandRegs));
+        // ---------------- codes to fp16 tiles: a thread to a row ----------------
+        const int wt = tid & 127;
+        Where &at = sh.where[3];
+        const Segment &seg = at.seg;
+        uint32_t entry = 0;
+        bool ok = true;
+        if (wt == 0) at.walk.begin(p, sh.share);
+        while (true) {
+            group_sync(2, 128);
+            if (wt == 0) at.more = at.walk.next(p, at.seg) ? 1 : 0;
+            group_sync(2, 128);
+            if (!at.more) break;
+            if (seg.w.bad) continue;
+            const int nb = static_cast<int>(seg.nb);
+            const int lag = rows_of(seg) > kTile ? 1 : 2;
+            const int64_t len = seg.w.len, b0 = seg.b0;
+            const uint32_t first_block = entry / 2;      // blocks of the segments before
+            for (int i = 0; ok && i < nb + lag; ++i)
+                for (int k = 0; k < 2; ++k) {            // values of block i - lag, keys of block i
+                    if (k == 0 ? i < lag : i >= nb) continue;
+                    const uint32_t r = entry % R::kRaw, slot = entry % R::kSlots;
+                    ok = ok && warp_wait_or_give_up(&b.raw_full[r], (entry / R::kRaw) & 1u, gave_up, p.status);
+                    const uint8_t *raw = smem + R::kRawAt + r * R::kRawBytes;
+                    if (ok && k == 1) {
+                        // this block's scales, fit for use: none past the end, finite ones
+                        // beside a list of the others
+                        const uint32_t kept = (first_block + static_cast<uint32_t>(i)) % R::kScales;
+                        const float *src = reinterpret_cast<const float *>(raw + R::kCodeBytes);
+                        float *dst = reinterpret_cast<float *>(smem + R::kScaleAt) + kept * 2 * kBlock;
+                        const bool there = (b0 + i) * kBlock + wt < len;
+                        const float kd = src[wt], vd = src[kBlock + wt];
+                        const bool finite = (__float_as_uint(vd) & 0x7f800000u) != 0x7f800000u;
+                        const float clean = there && finite ? vd : 0.0f;
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(clean) & 0x7fffffffu);
+                        const uint32_t odd = __ballot_sync(0xffffffffu, there && !finite);
+                        dst[wt] = kd;
+                        dst[kBlock + wt] = clean;
+                        if (lane == 0) {
+                            const int e = static_cast<int>(most >> 23) - 126;
+                            sh.exponent[kept][warp & 3] = e > 120 ? 120 : e;
+                            sh.odd[kept][warp & 3] = odd;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b.scale_full[kept]);
+                    }
+                    ok = ok && warp_wait_or_give_up(&b.kv_empty[slot], ((entry / R::kSlots) & 1u) ^ 1u, gave_up, p.status);
+                    if (!ok) break;
+                    // All of the row's codes first: no load can move above a store.
+                    uint8_t *dst = ring + slot * R::kTileBytes + wt * 128;
+                    uint4 codes[D / 16];
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c)   // as the copies' swizzle of 128 or 64 bytes has them
+                        codes[c] = *reinterpret_cast<const uint4 *>(
+                            raw + wt * D + ((D == 128 ? c ^ (wt & 7) : c ^ ((wt >> 1) & 3)) << 4));
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        const uint4 q = codes[c];
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                        uint32_t f[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            // a byte b ^ 0x80 under the exponent byte 0x64 is 1024 + 128 + code, exactly
+                            const uint32_t u = w[j] ^ 0x80808080u;
+                            const __half2 lo = __hsub2(as_h2(__byte_perm(u, 0x64646464u, 0x4140u)), as_h2(0x64806480u));
+                            const __half2 hi = __hsub2(as_h2(__byte_perm(u, 0x64646464u, 0x4342u)), as_h2(0x64806480u));
+                            f[2 * j] = *reinterpret_cast<const uint32_t *>(&lo);
+                            f[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&hi);
+                        }
+                        uint8_t *half = dst + (c >> 2) * R::kHalfBytes;
+                        *reinterpret_cast<uint4 *>(half + ((((2 * c) & 7) ^ (wt & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4 *>(half + ((((2 * c + 1) & 7) ^ (wt & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&b.raw_empty[r]);
+                        mbar_arrive(&b.kv_full[slot]);
+                    }
+                    ++entry;
+                }
+        }
+    } else if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
     if (warp == kCopyWarp) {
         // ---------------- copies: one lane to each box ----------------
         Where &at = sh.where[1];
@@ -341,23 +460,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.group = c0 >> 5;
                     a.next = load_ids(a.group + 1);
                 }
-                const uint32_t slot = entry % R::kSlots;
-                if (!warp_wait_or_give_up(&b.kv_empty[slot], ((entry / R::kSlots) & 1u) ^ 1u, gave_up, p.status)) {
+                // fp16 tiles land where they are used; codes in a ring of their own
+                const uint32_t slot = entry % kCopyRing;
+                uint64_t *full = KIND == kKvF16 ? &b.kv_full[slot] : &b.raw_full[slot];
+                uint64_t *empty = KIND == kKvF16 ? &b.kv_empty[slot] : &b.raw_empty[slot];
+                uint8_t *dst = KIND == kKvF16 ? ring + slot * R::kTileBytes : smem + R::kRawAt + slot * R::kRawBytes;
+                if (!warp_wait_or_give_up(empty, ((entry / kCopyRing) & 1u) ^ 1u, gave_up, p.status)) {
                     ok = false;
                     return;
                 }
-                // lane l: half l / chunks of chunk l % chunks
+                // lane l: kind l / chunks of chunk l % chunks (the 64-column halves of an fp16
+                // tile; or the codes and, with a block's keys, its key and value scales)
                 const int c = lane % chunks, h = lane / chunks;
                 const int id = __shfl_sync(0xffffffffu, a.cur, (c0 + c) & 31);
                 const uint32_t there = __ballot_sync(0xffffffffu, h == 0 && id >= 0);
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&b.kv_full[slot], __popc(there) * box_rows * 128 * R::kHalves);
+                const int row_bytes = KIND == kKvF16 ? 2 * D : (values ? D : D + 8);
+                if (lane == 0) mbar_arrive_expect_tx(full, __popc(there) * box_rows * row_bytes);
                 __syncwarp();
-                if (h < R::kHalves && id >= 0) {
-                    const int64_t j = (b0 + i) * kBlock + c * box_rows;
-                    copy_box(ring + slot * R::kTileBytes + h * R::kHalfBytes + c * box_rows * 128, values ? &vmap : &kmap,
-                             64 * h, y_head + (static_cast<int>(j & (page - 1)) & ~(box_rows - 1)), id,
-                             &b.kv_full[slot]);
+                const int64_t j = (b0 + i) * kBlock + c * box_rows;
+                const int y = y_head + (static_cast<int>(j & (page - 1)) & ~(box_rows - 1));
+                const CUtensorMap *map = values ? &vmap : &kmap;
+                if constexpr (KIND == kKvF16) {
+                    if (h < R::kHalves && id >= 0)
+                        copy_box(dst + h * R::kHalfBytes + c * box_rows * 128, map, 64 * h, y, id, full);
+                } else {
+                    if (h == 0 && id >= 0) copy_box(dst + c * box_rows * D, map, 0, y, id, full);
+                    if (!values && (h == 1 || h == 2) && id >= 0) {
+                        const float *src = (h == 1 ? p.k_scale : p.v_scale) + ((static_cast<int64_t>(id) * p.Hkv) << p.page_shift) + y;
+                        bulk_g2s(dst + R::kCodeBytes + (h - 1) * kBlock * 4 + c * box_rows * 4, src, box_rows * 4, full);
+                    }
                 }
                 __syncwarp();
                 ++entry;
@@ -368,8 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok && lane == 0)   // copies in flight land before the CTA leaves
-            for (uint32_t n = entry > R::kSlots ? entry - R::kSlots : 0u; n < entry; ++n)
-                mbar_wait_bounded(&b.kv_full[n % R::kSlots], (n / R::kSlots) & 1u, nullptr);
+            for (uint32_t n = entry > kCopyRing ? entry - kCopyRing : 0u; n < entry; ++n)
+                mbar_wait_bounded(KIND == kKvF16 ? &b.kv_full[n % kCopyRing] : &b.raw_full[n % kCopyRing],
+                                  (n / kCopyRing) & 1u, nullptr);
     } else if (warp == kMmaWarp) {
         // ---------------- products: the warp runs the loop, one elected lane issues ----------------
         constexpr uint32_t kScoreDesc = mma_desc(kBlock, false), kOutDesc = mma_desc(D, true);
@@ -453,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     } else {
         // ---------------- softmax: a thread to a row ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
         const int x = warp >> 2;                   // stream
         const int wt = tid & 127;                  // lane of tensor memory: row within the stream's tile
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -524,83 +656,132 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t rho = row_base + row;
             const int node = row < valid ? static_cast<int>(static_cast<uint32_t>(rho) / static_cast<uint32_t>(p.group)) : 0;
             const int32_t *tree_row = p.tree ? p.tree + (first_token + node) * p.tree_words : nullptr;
+            // A warp whose rows all lie past the last one leaves its weights as they are:
+            // what they give goes to rows that nobody reads.
+            const bool idle = row - lane >= valid;
             // Places below `open` are seen by every row of this stream.
             const int64_t open =
                 p.tree ? ctx : ctx + static_cast<uint32_t>(row_base + (two ? kTile * x : 0)) / static_cast<uint32_t>(p.group) + 1;
             float m = -INFINITY, l = 0.0f;
             bool first = true;
+            int ve = -126;                         // 8-bit rows: 2^ve is at least the largest value scale so far
             for (int i = two ? 0 : x; ok && i < nb; i += two ? 1 : 2, ns ^= 1u) {
                 const int64_t j0 = (b0 + i) * kBlock;
                 const bool masked = j0 + kBlock > open;
-                ok = warp_wait_or_give_up(&b.s_full[x], ns, gave_up, p.status);
+                const float *kd = nullptr, *vd = nullptr;   // 8-bit rows: the block's scales
+                float vfix = 1.0f, vunit = 1.0f;
+                if constexpr (KIND == kKvQ8) {
+                    const uint32_t block = entry / 2 + static_cast<uint32_t>(i), kept = block % R::kScales;
+                    ok = warp_wait_or_give_up(&b.scale_full[kept], (block / R::kScales) & 1u, gave_up, p.status);
+                    kd = reinterpret_cast<const float *>(smem + R::kScaleAt) + kept * 2 * kBlock;
+                    vd = kd + kBlock;
+                    int e = sh.exponent[kept][0];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w) e = sh.exponent[kept][w] > e ? sh.exponent[kept][w] : e;
+                    if (e > ve) {
+                        vfix = exp2_fast(static_cast<float>(ve - e));
+                        ve = e;
+                    }
+                    vunit = power_of_2(-ve);
+                    // a value scale that is not finite makes the rows that see it NaN
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t odd = sh.odd[kept][w];
+                        if (odd && (odd & seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 32 * w)))
+                            l = __int_as_float(0x7fffffff);
+                    }
+                }
+                ok = ok && warp_wait_or_give_up(&b.s_full[x], ns, gave_up, p.status);
                 if (!ok) break;
                 fence_after();
                 // The scores were issued after every earlier product of the stream:
                 // its outputs are at rest until this block's first weights are given.
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t s[64];
-                    ld_32cols(s_at + 64 * h, s);
-                    ld_32cols(s_at + 64 * h + 32, s + 32);
-                    ld_wait(s);
-                    ld_wait(s + 32);
-                    if (masked) {
+                    if (!idle) {
+                        uint32_t s[64];
+                        ld_32cols(s_at + 64 * h, s);
+                        ld_32cols(s_at + 64 * h + 32, s + 32);
+                        ld_wait(s);
+                        ld_wait(s + 32);
+                        if constexpr (KIND == kKvQ8) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint32_t see =
-                                seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 64 * h + 32 * c);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u;   // -inf
-                        }
-                    }
-                    uint32_t w[32];
-                    uint64_t sum[2];
-                    // Weights by the maximum so far, beside the maximum of these
-                    // scores; where one lies past the lag, the outputs follow the new
-                    // maximum and the weights are taken again.
-                    while (true) {
-                        const float c0 = kShift - (m == -INFINITY ? 0.0f : m);
-                        const uint64_t scale2 = pair(scale, scale), c2 = pair(c0, c0);
-                        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        sum[0] = sum[1] = 0ull;
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
-                            const uint64_t e = fma2(pair(s0, s1), scale2, c2);
-                            const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
-                            sum[k & 1] = add2(sum[k & 1], pair(a, c));
-                            w[k] = float2_to_half2_bits(make_float2(a, c));
-                            t[k & 3] = fmaxf(t[k & 3], fmaxf(s0, s1));
-                        }
-                        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
-                        const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
-                        if (!__any_sync(0xffffffffu, rises)) break;
-                        if (!first) {
-                            if (h == 1) {
-                                ok = warp_wait_or_give_up(&b.o_full[x][0], ns, gave_up, p.status);
-                                if (!ok) break;
-                                fence_after();
+                            for (int k = 0; k < 64; k += 4) {
+                                const float4 d = *reinterpret_cast<const float4 *>(kd + 64 * h + k);
+                                const uint64_t a = mul2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), pair(d.x, d.y));
+                                const uint64_t c = mul2(pair(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), pair(d.z, d.w));
+                                s[k] = __float_as_uint(low(a));
+                                s[k + 1] = __float_as_uint(high(a));
+                                s[k + 2] = __float_as_uint(low(c));
+                                s[k + 3] = __float_as_uint(high(c));
                             }
-                            const float f = rises ? exp2_fast(m - top) : 1.0f;
-                            l *= f;
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t see =
+                                    seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 64 * h + 32 * c);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u;   // -inf
+                            }
+                        }
+                        uint32_t w[32];
+                        uint64_t sum[2];
+                        // Weights by the maximum so far, beside the maximum of these
+                        // scores; where one lies past the lag, the outputs follow the new
+                        // maximum and the weights are taken again.
+                        while (true) {
+                            const float c0 = kShift - (m == -INFINITY ? 0.0f : m);
+                            const uint64_t scale2 = pair(scale, scale), c2 = pair(c0, c0);
+                            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            sum[0] = sum[1] = 0ull;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
+                                const uint64_t e = fma2(pair(s0, s1), scale2, c2);
+                                const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
+                                sum[k & 1] = add2(sum[k & 1], pair(a, c));
+                                if constexpr (KIND == kKvQ8) {
+                                    const float2 d = *reinterpret_cast<const float2 *>(vd + 64 * h + 2 * k);
+                                    const uint64_t g = mul2(pair(a, c), mul2(pair(d.x, d.y), pair(vunit, vunit)));
+                                    w[k] = float2_to_half2_bits(make_float2(low(g), high(g)));
+                                } else {
+                                    w[k] = float2_to_half2_bits(make_float2(a, c));
+                                }
+                                t[k & 3] = fmaxf(t[k & 3], fmaxf(s0, s1));
+                            }
+                            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+                            const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
+                            if (!__any_sync(0xffffffffu, rises) && vfix == 1.0f) break;
+                            if (!first) {
+                                if (h == 1) {
+                                    ok = warp_wait_or_give_up(&b.o_full[x][0], ns, gave_up, p.status);
+                                    if (!ok) break;
+                                    fence_after();
+                                }
+                                float f = rises ? exp2_fast(m - top) : 1.0f;
+                                l *= f;
+                                f *= vfix;
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t v[32];
-                                ld_32cols(o_at + 32 * c, v);
-                                ld_wait(v);
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t v[32];
+                                    ld_32cols(o_at + 32 * c, v);
+                                    ld_wait(v);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                                st_32cols(o_at + 32 * c, v);
+                                    for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                                    st_32cols(o_at + 32 * c, v);
+                                }
                             }
+                            if (rises) m = top;
+                            vfix = 1.0f;
                         }
-                        if (rises) m = top;
+                        if (!ok) break;
+                        st_32cols(s_at + 64 * h, w);
+                        sum[0] = add2(sum[0], sum[1]);
+                        l += low(sum[0]) + high(sum[0]);
                     }
-                    if (!ok) break;
-                    st_32cols(s_at + 64 * h, w);
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += low(sum[0]) + high(sum[0]);
-                    if (masked && (wt >> 6) == h && j0 + wt >= ctx) {
+                    if (KIND == kKvF16 && masked && (wt >> 6) == h && j0 + wt >= ctx) {
                         // Value rows past the end are cleared, and so are nodes' rows
                         // that are not finite (add_strange_nodes adds those).
                         const uint32_t e = entry + seq_v(i, lag, nb);
@@ -655,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (x == 1) {
                     sh.m[wt] = m;
                     sh.l[wt] = l;
+                    if (wt == 0) sh.ve = ve;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
@@ -674,10 +856,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 group_sync(1, 256);
             }
-            const bool whole = seg.nb == seg.blocks;
+            const bool whole = seg.whole;
             float *part = whole ? nullptr : workspace_partial(p, blockIdx.x, seg.b0 == 0 ? 1 : 0, kRows, D);
             if (two || x == 0) {
                 float f1 = 0.0f;
+                if (KIND == kKvQ8 && two) f = power_of_2(ve);
                 if (!two) {
                     const float m1 = sh.m[wt], top = fmaxf(m, m1);
                     f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
@@ -685,10 +868,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float l1 = sh.l[wt];
                     l = (m == -INFINITY ? l : l * f) + (m1 == -INFINITY ? l1 : l1 * f1);
                     m = top;
+                    if constexpr (KIND == kKvQ8) {
+                        f *= power_of_2(ve);
+                        f1 *= power_of_2(sh.ve);
+                    }
                 }
                 const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
                 const __half *q = nullptr;
-                if (strange && row < valid && !seg.w.bad)
+                if (KIND == kKvF16 && strange && row < valid && !seg.w.bad)
                     q = p.q + (first_token + node) * p.q_stride + (seg.kvh * p.group + (rho - static_cast<int64_t>(node) * p.group)) * D;
                 if (!whole && row < valid) {
                     part[row] = m;
@@ -732,9 +919,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (tid == 0 && !whole && seg.b0 == 0) {
+            if (tid == 0 && seg.parts > 0) {
                 left_unit = true;
-                leave_unit(p, seg, sh.share, valid, first_token);
+                leave_unit(p, seg, valid, first_token);
             }
             if (tid == 0) sh.strange = 0;
             fence_before();
@@ -751,24 +938,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, int KIND>
 cudaError_t launch_with(const AttnParams &p, int sms, cudaStream_t s, bool pdl)
 {
     const int page = 1 << p.page_shift;
     const int rows = page < kBlock ? page : kBlock;
     CUtensorMap kmap, vmap;
-    if (!encode_rows(&kmap, p, p.k, D, kKvF16, rows) || !encode_rows(&vmap, p, p.v, D, kKvF16, rows))
+    using R = Ring<D, KIND>;
+    if (!encode_rows(&kmap, p, p.k, D, KIND, rows) || !encode_rows(&vmap, p, p.v, D, KIND, rows))
         return cudaErrorInvalidValue;
-    auto kernel = tree_attn_tiles_kernel<D>;
-    cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(kernel), Ring<D>::kSmem);
+    auto kernel = tree_attn_tiles_kernel<D, KIND>;
+    cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(kernel), R::kSmem);
     if (e != cudaSuccess) return e;
     // The softmax groups' share of the registers exists only if the launch brings it.
     static const int regs = [] {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, tree_attn_tiles_kernel<D>) == cudaSuccess ? a.numRegs : 0;
+        return cudaFuncGetAttributes(&a, tree_attn_tiles_kernel<D, KIND>) == cudaSuccess ? a.numRegs : 0;
     }();
-    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = launch_ex(kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads), Ring<D>::kSmem, s, pdl, kmap, vmap, p);
+    if (regs < R::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = launch_ex(kernel, dim3(static_cast<unsigned>(sms)), dim3(R::kThreads), R::kSmem, s, pdl, kmap, vmap, p);
     if (e != cudaSuccess) return e;
     return launch_join<kRows, D>(p, sms, kBlock, s, pdl);
 }
@@ -777,10 +965,11 @@ cudaError_t launch_with(const AttnParams &p, int sms, cudaStream_t s, bool pdl)
 
 int64_t attn_tiles_workspace_floats(int sms) { return 2 * static_cast<int64_t>(sms) * partial_floats(kRows, 128); }
 
-cudaError_t launch_attn_tiles(const AttnParams &p, int D, int, int sms, cudaStream_t s, bool pdl)
+cudaError_t launch_attn_tiles(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl)
 {
     if (sms > kMaxGrid) return cudaErrorInvalidConfiguration;
-    return D == 64 ? launch_with<64>(p, sms, s, pdl) : launch_with<128>(p, sms, s, pdl);
+    if (D == 64) return kind == kKvF16 ? launch_with<64, kKvF16>(p, sms, s, pdl) : launch_with<64, kKvQ8>(p, sms, s, pdl);
+    return kind == kKvF16 ? launch_with<128, kKvF16>(p, sms, s, pdl) : launch_with<128, kKvQ8>(p, sms, s, pdl);
 }
 
 }  // namespace qmv
