@@ -199,14 +199,14 @@ def qmv_read_probe_ptr(buf: int, nbytes: int, out: int, stream: int = 0) -> None
 
 # -- torch-tensor entry points ---------------------------------------------------------
 
-_torch_module = None
+_torch_module = _int32_type = None
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _int32_type
     if _torch_module is None:
         import torch
-        _torch_module = torch
+        _torch_module, _int32_type = torch, torch.int32
     return _torch_module
 
 
@@ -480,7 +480,7 @@ class KvCache:
     scale to a row, k_scale and v_scale [n_pages, kv_heads, page]).  The rows of a page are dense; pages may lie
     apart by any stride the two share (k and v interleaved in one buffer, for instance)."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads", "page", "head_dim", "kind", "device", "_args")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads", "page", "head_dim", "kind", "device", "index", "_args")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         torch = _torch()
@@ -503,7 +503,7 @@ class KvCache:
                 raise ValueError("KvCache: scales must be contiguous float32 [n_pages, kv_heads, page] beside k and v")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.kv_heads, self.page, self.head_dim = n_pages, heads, page, dim
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         stride = k.stride(0) if n_pages > 1 else heads * page * dim
         self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else 0,
                       v_scale.data_ptr() if v_scale is not None else 0, stride)
@@ -542,18 +542,16 @@ def _on(fn, name, t, index):
 
 
 def _int32(fn, name, t, dim, index):
-    if t.get_device() != index or index < 0:
-        _on(fn, name, t, index)
+    if t.get_device() == index and t.dtype is _int32_type and t.dim() == dim and t.is_contiguous() and index >= 0:
+        return t.data_ptr()
+    _on(fn, name, t, index)
+    if index < 0:
         raise TypeError(f"{fn}: {name} must be a CUDA tensor (no CPU path)")
-    if t.dtype is not _torch().int32 or t.dim() != dim or not t.is_contiguous():
-        raise TypeError(f"{fn}: {name} must be a contiguous int32 tensor with {dim} dimension" + ("s" if dim > 1 else ""))
-    return t.data_ptr()
+    raise TypeError(f"{fn}: {name} must be a contiguous int32 tensor with {dim} dimension" + ("s" if dim > 1 else ""))
 
 
 def _tree_args(fn, tree, tokens, index):
-    """(address, words) of a tree mask [tokens, words], (0, 0) for none."""
-    if tree is None:
-        return 0, 0
+    """(address, words) of a tree mask [tokens, words]."""
     ptr = _int32(fn, "tree", tree, 2, index)
     if tree.shape[0] != tokens or (tree.shape[1] == 0 and tokens > 0):
         raise ValueError(f"{fn}: tree must have a row of at least one word for each of the {tokens} tokens")
@@ -594,7 +592,7 @@ def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n
         head_ptr = _int32(fn, "head", head, 1, at)
         if head.shape[0] != 1:
             raise ValueError(f"{fn}: head must be one number")
-    tree_ptr, words = _tree_args(fn, tree, tokens, at)
+    tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, tokens, at)
     out = torch.empty(2 * R + 2 + 3 * tokens, dtype=torch.int32, device=lens.device)
     o, n = out.data_ptr(), 4 * tokens
     s = o + 4 * (2 * R + 1)
@@ -612,23 +610,26 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
     torch = _torch()
     fn = "qmv_kv_append"
     at = qkv.get_device()
-    _on(fn, "cache", cache.k, at)
+    if at != cache.index or at < 0:
+        _on(fn, "cache", cache.k, at)
+        raise TypeError(f"{fn}: qkv must be a CUDA tensor (no CPU path)")
     f32 = qkv.dtype is torch.float32
     if not f32 and qkv.dtype is not torch.float16:
         raise TypeError(f"{fn}: qkv must be float32 or float16")
     hk, D = cache.kv_heads, cache.head_dim
-    if qkv.dim() != 2 or qkv.shape[1] != (n_heads + 2 * hk) * D or (qkv.shape[0] and qkv.stride(1) != 1):
+    shape, apart = qkv.shape, qkv.stride()
+    if len(shape) != 2 or shape[1] != (n_heads + 2 * hk) * D or (apart[1] != 1 and shape[0]):
         raise ValueError(f"{fn}: qkv must be [T, (n_heads + 2 * {hk}) * {D}] with dense rows")
-    T, wide = qkv.shape
+    T, wide = shape
     slots_ptr = _int32(fn, "slots", slots, 1, at)
-    if slots.shape[0] != T:
+    if len(slots) != T:
         raise ValueError(f"{fn}: one slot to a token")
     pos_ptr = cos_ptr = sin_ptr = n_pos = rot = 0
     if (cos is None) != (sin is None) or (cos is not None and pos is None):
         raise ValueError(f"{fn}: a rotation takes pos, cos and sin")
     if cos is not None:
         pos_ptr = _int32(fn, "pos", pos, 1, at)
-        if pos.shape[0] != T:
+        if len(pos) != T:
             raise ValueError(f"{fn}: one position to a token")
         if not (cos.get_device() == sin.get_device() == at and cos.dtype is torch.float32 and sin.dtype is torch.float32
                 and cos.dim() == 2 and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous()):
@@ -637,12 +638,12 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
         rot *= 2
         cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
     if q is None:
-        q = torch.empty((T, n_heads, D), dtype=torch.float16, device=qkv.device)
+        q = torch.empty((T, n_heads, D), dtype=torch.float16, device=cache.device)
     elif not (q.get_device() == at and q.dtype is torch.float16 and q.is_contiguous() and q.numel() == T * n_heads * D):
         raise ValueError(f"{fn}: q must be a contiguous CUDA float16 tensor of {T}x{n_heads}x{D}")
     k, v, ks, vs, page_stride = cache._args
     _call_on(fn, at, stream,
-             (qkv.data_ptr(), qkv.stride(0) if T > 1 else wide, f32, slots_ptr, pos_ptr, cos_ptr, sin_ptr, n_pos, rot,
+             (qkv.data_ptr(), apart[0] if T > 1 else wide, f32, slots_ptr, pos_ptr, cos_ptr, sin_ptr, n_pos, rot,
               bool(interleaved), q.data_ptr(), k, v, ks, vs, cache.kind, T, int(n_heads), hk, D, cache.n_pages,
               cache.page, page_stride))
     return q
@@ -668,31 +669,34 @@ def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=Non
     torch = _torch()
     fn = "qmv_tree_attn"
     at = q.get_device()
-    _on(fn, "cache", cache.k, at)
+    if at != cache.index or at < 0:
+        _on(fn, "cache", cache.k, at)
+        raise TypeError(f"{fn}: q must be a CUDA tensor (no CPU path)")
     if q.dtype is not torch.float16:
         raise TypeError(f"{fn}: q must be float16")
     D = cache.head_dim
-    if q.dim() != 3 or q.shape[2] != D or (q.numel() and (q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != D))):
+    shape, apart = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != D or ((apart[2] != 1 or (apart[1] != D and shape[1] > 1)) and q.numel()):
         raise ValueError(f"{fn}: q must be [T, heads, {D}] with dense rows")
-    T, H, _ = q.shape
-    table_ptr, start_ptr, len_ptr = _int32(fn, "table", table, 2, at), _int32(fn, "start", start, 1, at), \
-        _int32(fn, "kv_len", kv_len, 1, at)
+    T, H, _ = shape
+    table_ptr, start_ptr = _int32(fn, "table", table, 2, at), _int32(fn, "start", start, 1, at)
     R, width = table.shape
-    if start.shape[0] != R + 1 or kv_len.shape[0] != R:
+    len_ptr = _int32(fn, "kv_len", kv_len, 1, at)
+    if len(start) != R + 1 or len(kv_len) != R:
         raise ValueError(f"{fn}: table [R, width], start [R + 1] and kv_len [R] must agree")
-    tree_ptr, words = _tree_args(fn, tree, T, at)
+    tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, T, at)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float16, device=q.device)
+        out = torch.empty(shape, dtype=torch.float16, device=cache.device)
     elif not (out.get_device() == at and out.dtype is torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
         raise ValueError(f"{fn}: out must be a contiguous CUDA float16 tensor of {T}x{H}x{D}")
     if workspace is None:
-        workspace = qmv_tree_attn_workspace(q.device)
-    elif not (workspace.get_device() == at and workspace.is_contiguous()):
+        workspace = qmv_tree_attn_workspace(cache.device)
+    elif workspace.get_device() != at or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
     k, v, ks, vs, page_stride = cache._args
     _call_on(fn, at, stream,
-             (q.data_ptr(), q.stride(0) if T > 1 else H * D, k, v, ks, vs, cache.kind, cache.n_pages, cache.page,
+             (q.data_ptr(), apart[0] if T > 1 else H * D, k, v, ks, vs, cache.kind, cache.n_pages, cache.page,
               page_stride, table_ptr, width, start_ptr, len_ptr, tree_ptr, words,
               None if scale is None else ctypes.byref(ctypes.c_float(scale)), out.data_ptr(), workspace.data_ptr(),
-              workspace.numel() * workspace.element_size(), R, T, H, cache.kv_heads, D))
+              workspace.nbytes, R, T, H, cache.kv_heads, D))
     return out

@@ -476,7 +476,7 @@ cudaError_t launch_join(const AttnParams &p, int grid, int block, cudaStream_t s
 {
     if ((p.width << p.page_shift) <= block) return cudaSuccess;
     // 32 rows: 16 runs of pieces; 256 rows: a block to each CTA, 16 runs of 256
-    constexpr int kCtas = ROWS > 64 ? 1 : 8, kRuns = ROWS * D / 8 / 32 < 16 ? ROWS * D / 8 / 32 : 16;
+    constexpr int kCtas = ROWS > 64 ? 1 : 2, kRuns = ROWS * D / 8 / 32 < 16 ? ROWS * D / 8 / 32 : 16;
     return launch_ex(join_units_kernel<ROWS, D, kCtas>, dim3((grid + kCtas - 1) / kCtas, kRuns), dim3(kJoinThreads), 0, s, pdl,
                      p, grid);
 }

@@ -18,8 +18,8 @@
 // maximum and sum need no exchange.  The output in tensor memory is rescaled
 // only where a row's maximum has risen by more than 2^5 since it last was; until
 // then the weights simply come out larger, p <= 2^(10 + 5) < 65504.
-//   Warps: 0-3 and 4-7 the two softmax groups, 8 issues the products, 9 the
-// copies.  All waits are bounded.
+//   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
+// the copies.  All waits are bounded.
 #include <cstdint>
 
 #include "qmv_attn.cuh"
@@ -33,7 +33,7 @@ constexpr int kTile = 128;           // rows of a stream
 constexpr int kRows = 2 * kTile;     // rows of a unit
 constexpr int kBlock = 128;          // places of a block
 constexpr int kCost = 6;             // what a unit costs besides its blocks, in blocks
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kMmaWarp = 8, kCopyWarp = 9;   // and 10: the second stream's products
 constexpr int kExpandWarp = 12;      // 12-15, for 8-bit rows only
 constexpr float kShift = 10.0f;      // weights are 2^10 times exp(s - max)
 constexpr float kLazy = 5.0f;        // a maximum may lag this far (log2)
@@ -218,10 +218,10 @@ struct Barriers {
     uint64_t raw_full[8], raw_empty[8];   // 8-bit rows: the copies' ring of codes
     uint64_t scale_full[16];              // and the blocks' scales
     uint64_t q_full;          // queries of a segment are in shared memory, the last outputs read
-    uint64_t s_full[2];       // a stream's scores of a block are in tensor memory
+    uint64_t s_full[2][2];    // a half of a stream's scores is in tensor memory
     uint64_t p_full[2][2];    // a half of its weights is
     uint64_t o_full[2][2];    // that half's product with values is done
-    uint64_t drain;           // (after a wait ran out) the products in flight are done
+    uint64_t drain[2];        // (after a wait ran out) the stream's products in flight are done
 };
 
 // Where a role is: one of its threads walks, and the segment lies in shared
@@ -245,7 +245,7 @@ struct Shared {
     uint32_t tmem;
     int gave_up;              // volatile use: a wait ran out somewhere
     int strange;              // a value row of the segment's nodes is not finite
-    Where where[4];           // the softmax groups, the copies, the products, the expanding warps
+    Where where[5];           // the softmax groups, the streams' products, the copies, the expanding warps
     float m[kTile], l[kTile];
     int ve;
     // 8-bit rows, of each block kept: by 32 places, which value scales are not
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         prefetch_map(&vmap);
         for (int i = 0; i < R::kSlots; ++i) {
             mbar_init(&b.kv_full[i], KIND == kKvF16 ? 1 : 4);
-            mbar_init(&b.kv_empty[i], 1);
+            mbar_init(&b.kv_empty[i], 2);
         }
         for (int i = 0; KIND == kKvQ8 && i < R::kRaw; ++i) {
             mbar_init(&b.raw_full[i], 1);
@@ -310,13 +310,13 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         for (int i = 0; KIND == kKvQ8 && i < R::kScales; ++i) mbar_init(&b.scale_full[i], 4);
         mbar_init(&b.q_full, 8);
         for (int x = 0; x < 2; ++x) {
-            mbar_init(&b.s_full[x], 1);
+            mbar_init(&b.drain[x], 1);
             for (int h = 0; h < 2; ++h) {
+                mbar_init(&b.s_full[x][h], 1);
                 mbar_init(&b.p_full[x][h], 4);
                 mbar_init(&b.o_full[x][h], 1);
             }
         }
-        mbar_init(&b.drain, 1);
         sh.gave_up = 0;
         sh.strange = 0;
         mbar_init_fence();
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
     fence_after();
     const uint32_t tmem = sh.tmem;
     constexpr uint32_t kCopyRing = KIND == kKvF16 ? R::kSlots : R::kRaw;
-    // Columns: scores of stream x (its weights over them) at 128 x, outputs at 256 + D x.
+    // Columns: scores of stream x (its weights over them, half by half) at 128 x,
+    // outputs at 256 + D x.
 
     auto rows_of = [&](const Segment &s) -> int {
         const int64_t left = static_cast<int64_t>(s.w.nodes) * p.group - static_cast<int64_t>(s.tile) * kRows;
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kExpandRegs));
         // ---------------- codes to fp16 tiles: a thread to a row ----------------
         const int wt = tid & 127;
-        Where &at = sh.where[3];
+        Where &at = sh.where[4];
         const Segment &seg = at.seg;
         uint32_t entry = 0;
         bool ok = true;
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kOtherRegs));
     if (warp == kCopyWarp) {
         // ---------------- copies: one lane to each box ----------------
-        Where &at = sh.where[1];
+        Where &at = sh.where[3];
         const Segment &seg = at.seg;
         if (lane == 0) at.walk.begin(p, sh.share);
         const int page = 1 << p.page_shift;
@@ -502,15 +503,17 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             for (uint32_t n = entry > kCopyRing ? entry - kCopyRing : 0u; n < entry; ++n)
                 mbar_wait_bounded(KIND == kKvF16 ? &b.kv_full[n % kCopyRing] : &b.raw_full[n % kCopyRing],
                                   (n / kCopyRing) & 1u, nullptr);
-    } else if (warp == kMmaWarp) {
-        // ---------------- products: the warp runs the loop, one elected lane issues ----------------
-        constexpr uint32_t kScoreDesc = mma_desc(kBlock, false), kOutDesc = mma_desc(D, true);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 2) {
+        // ---------------- products: a warp to each stream runs the loop, one elected lane issues ----------------
+        const int x = (warp - kMmaWarp) >> 1;
+        constexpr uint32_t kScoreDesc = mma_desc(64, false), kOutDesc = mma_desc(D, true);
         const uint64_t qd = tile_desc(smem_u32(qbuf), 16), kd = tile_desc(smem_u32(ring), 16);
         const uint64_t vd = tile_desc(smem_u32(ring), R::kHalfBytes);
-        Where &at = sh.where[2];
+        const uint32_t s_at = tmem + 128 * x, o_at = tmem + 256 + D * x;
+        Where &at = sh.where[1 + x];
         const Segment &seg = at.seg;
         if (lane == 0) at.walk.begin(p, sh.share);
-        uint32_t entry = 0, segs = 0, np = 0, commits = 0;   // np: the phases of p_full, a bit to a stream
+        uint32_t entry = 0, segs = 0, np = 0, commits = 0;   // np: phase of this stream's blocks
         bool ok = true;
         while (ok && at.next_for_warp(p)) {
             if (seg.w.bad) continue;   // nothing to multiply, its outputs are NaN
@@ -521,65 +524,80 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             fence_after();
             const int nb = static_cast<int>(seg.nb);
             const bool two = rows_of(seg) > kTile;
-            const int lag = two ? 1 : 2;
+            const int lag = two ? 1 : 2, step = lag;
+            const uint64_t qx = qd + (two ? x : 0) * (R::kTileBytes >> 4);
             auto wait_tile = [&](uint32_t n) {
                 const uint32_t e = entry + n;
                 ok = ok && warp_wait_or_give_up(&b.kv_full[e % R::kSlots], (e / R::kSlots) & 1u, gave_up, p.status);
                 return static_cast<uint64_t>((e % R::kSlots) * (R::kTileBytes >> 4));
             };
-            for (int i = 0; ok && i < nb + lag; ++i) {
-                const uint32_t sv = i >= lag ? seq_v(i - lag, lag, nb) : 0u, sk = seq_k(i, lag);
-                for (int x = two ? 0 : (i & 1); ok && x < (two ? 2 : (i & 1) + 1); ++x) {
-                    const bool last_use = !two || x == 1;
-                    if (i >= lag) {
-                        // o_x += p v of block i - lag, each half as its weights arrive
-                        const uint64_t off = wait_tile(sv);
+            // Both streams' products free a slot; a stream that has the block alone does it twice.
+            auto free_tile = [&](uint32_t n) {
+                uint64_t *empty = &b.kv_empty[(entry + n) % R::kSlots];
+                mma_commit(empty);
+                if (!two) mma_commit(empty);
+            };
+            // s = q k^T of half h of a block (64 places).
+            auto scores = [&](uint64_t off, uint32_t sk, int h) {
+                if (elect_one()) {
+                    const uint64_t kx = kd + off + h * (64 * 128 >> 4);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            ok = ok && warp_wait_or_give_up(&b.p_full[x][h], (np >> x) & 1u, gave_up, p.status);
-                            if (!ok) break;
-                            fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                                    mma_ts(tmem + 256 + D * x, tmem + 128 * x + 64 * h + 8 * (ks - 4 * h),
-                                           vd + off + ks * (2048 >> 4), kOutDesc, i >= 2 * lag || ks > 0);
-                                mma_commit(&b.o_full[x][h]);
-                                if (h == 1 && last_use) mma_commit(&b.kv_empty[(entry + sv) % R::kSlots]);
-                            }
-                            __syncwarp();
-                            ++commits;
-                        }
-                        np ^= 1u << x;
-                        if (!ok) break;
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t k16 = (ks >> 2) * (R::kHalfBytes >> 4) + (ks & 3) * 2;
+                        mma_ss(s_at + 64 * h, qx + k16, kx + k16, kScoreDesc, ks > 0);
                     }
-                    if (i < nb) {
-                        // s_x = q_x k^T of block i, over the weights that the products just
-                        // issued read first (the products of a CTA run in the order of issue)
-                        const uint64_t off = wait_tile(sk);
+                    mma_commit(&b.s_full[x][h]);
+                    if (h == 1) free_tile(sk);
+                }
+                __syncwarp();
+                ++commits;
+            };
+            const int i0 = two ? 0 : x;
+            if (i0 < nb) {
+                const uint32_t sk = seq_k(i0, lag);
+                const uint64_t off = wait_tile(sk);
+                if (!ok) break;
+                fence_after();
+                scores(off, sk, 0);
+                scores(off, sk, 1);
+            }
+            for (int i = i0; ok && i < nb; i += step, np ^= 1u) {
+                const uint32_t sv = seq_v(i, lag, nb), sk = seq_k(i + step, lag);
+                const bool more = i + step < nb;
+                const uint64_t v_off = wait_tile(sv);
+                uint64_t k_off = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // o += p v, half a block, as its weights arrive
+                    ok = ok && warp_wait_or_give_up(&b.p_full[x][h], np, gave_up, p.status);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                            mma_ts(o_at, s_at + 64 * h + 8 * (ks - 4 * h), vd + v_off + ks * (2048 >> 4),
+                                   kOutDesc, i > i0 || ks > 0);
+                        mma_commit(&b.o_full[x][h]);
+                        if (h == 1) free_tile(sv);
+                    }
+                    __syncwarp();
+                    ++commits;
+                    // that half's scores of the next block, over the weights that the product
+                    // just issued reads first (a thread's products run in the order of issue)
+                    if (more) {
+                        if (h == 0) k_off = wait_tile(sk);
                         if (!ok) break;
                         fence_after();
-                        if (elect_one()) {
-                            const uint64_t qx = qd + (two ? x : 0) * (R::kTileBytes >> 4);
-#pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint32_t step = (ks >> 2) * (R::kHalfBytes >> 4) + (ks & 3) * 2;
-                                mma_ss(tmem + 128 * x, qx + step, kd + off + step, kScoreDesc, ks > 0);
-                            }
-                            mma_commit(&b.s_full[x]);
-                            if (last_use) mma_commit(&b.kv_empty[(entry + sk) % R::kSlots]);
-                        }
-                        __syncwarp();
-                        ++commits;
+                        scores(k_off, sk, h);
                     }
                 }
             }
             entry += 2u * static_cast<uint32_t>(nb);
         }
         if (!ok && commits > 0) {   // products in flight end before the tensor memory is given back
-            if (elect_one()) mma_commit(&b.drain);
+            if (elect_one()) mma_commit(&b.drain[x]);
             __syncwarp();
-            if (lane == 0) mbar_wait_bounded(&b.drain, 0, nullptr);
+            if (lane == 0) mbar_wait_bounded(&b.drain[x], 0, nullptr);
             __syncwarp();
         }
     }
@@ -691,13 +709,11 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                             l = __int_as_float(0x7fffffff);
                     }
                 }
-                ok = ok && warp_wait_or_give_up(&b.s_full[x], ns, gave_up, p.status);
-                if (!ok) break;
-                fence_after();
-                // The scores were issued after every earlier product of the stream:
-                // its outputs are at rest until this block's first weights are given.
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
+                    ok = ok && warp_wait_or_give_up(&b.s_full[x][h], ns, gave_up, p.status);
+                    if (!ok) break;
+                    fence_after();
                     if (!idle) {
                         uint32_t s[64];
                         ld_32cols(s_at + 64 * h, s);
@@ -755,11 +771,10 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                             const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
                             if (!__any_sync(0xffffffffu, rises) && vfix == 1.0f) break;
                             if (!first) {
-                                if (h == 1) {
-                                    ok = warp_wait_or_give_up(&b.o_full[x][0], ns, gave_up, p.status);
-                                    if (!ok) break;
-                                    fence_after();
-                                }
+                                // of the products before these weights only the last may still run
+                                ok = warp_wait_or_give_up(&b.o_full[x][1 - h], h == 1 ? ns : ns ^ 1u, gave_up, p.status);
+                                if (!ok) break;
+                                fence_after();
                                 float f = rises ? exp2_fast(m - top) : 1.0f;
                                 l *= f;
                                 f *= vfix;
