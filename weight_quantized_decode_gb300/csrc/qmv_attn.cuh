@@ -30,7 +30,7 @@ namespace qmv {
 
 // a / b for a, b >= 0, in 32 bits where they fit (a 64-bit division is a long
 // sequence of dependent instructions).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
     if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
     return a / b;
@@ -49,19 +49,19 @@ struct RequestWork {
 // Entries of the unit of row tile `tile`: COST and its blocks.  CUT: the rows of a chain see nothing
 // past the tile's last token, and the blocks there are left out.
 template <int ROWS, int BLOCK, int COST, bool CUT>
-__device__ __forceinline__ int64_t unit_entries(const AttnParams &p, const RequestWork &w, int tile)
+__host__ __device__ __forceinline__ int64_t unit_entries(const AttnParams &p, const RequestWork &w, int tile)
 {
     if (w.bad) return COST + 1;
     int64_t places = w.len;
     if (CUT && !p.tree) {
-        const int64_t last = quotient((static_cast<int64_t>(tile) + 1) * ROWS - 1, p.group);   // the tile's last token
-        if (last < w.nodes) places = w.len - w.nodes + last + 1;
+        const uint32_t last = ((static_cast<uint32_t>(tile) + 1) * ROWS - 1) / static_cast<uint32_t>(p.group);   // the tile's last token
+        if (last < static_cast<uint32_t>(w.nodes)) places = w.len - w.nodes + last + 1;
     }
     return COST + (places + BLOCK - 1) / BLOCK;
 }
 
 template <int ROWS, int BLOCK, int COST, bool CUT>
-__device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t r)
+__host__ __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t r)
 {
     RequestWork w;
     // offsets past the T rows of q are cut off
@@ -72,9 +72,22 @@ __device__ __forceinline__ RequestWork request_work(const AttnParams &p, int64_t
     w.bad = lo < 0 || hi > p.T || w.len < w.nodes || w.len > (p.width << p.page_shift);
     if (w.bad) w.len = 0;
     w.tiles = static_cast<int>((static_cast<int64_t>(w.nodes) * p.group + ROWS - 1) / ROWS);
-    if (CUT && !p.tree) {
+    if (CUT && !p.tree && !w.bad) {
+        // the tiles' last tokens, ((t + 1) * ROWS - 1) / group, without the divisions
+        const uint32_t group = static_cast<uint32_t>(p.group), by = ROWS / group, over = ROWS % group;
+        uint32_t last = (ROWS - 1) / group, rest = (ROWS - 1) % group;
+        const int64_t ctx = w.len - w.nodes;
         w.per_head = 0;
-        for (int t = 0; t < w.tiles; ++t) w.per_head += unit_entries<ROWS, BLOCK, COST, CUT>(p, w, t);
+        for (int t = 0; t < w.tiles; ++t) {
+            const int64_t places = ctx + (last < static_cast<uint32_t>(w.nodes) ? last + 1 : w.nodes);
+            w.per_head += COST + static_cast<int64_t>(static_cast<uint64_t>(places + BLOCK - 1) / BLOCK);
+            last += by;
+            rest += over;
+            if (rest >= group) {
+                rest -= group;
+                ++last;
+            }
+        }
     } else {
         w.per_head = w.tiles * unit_entries<ROWS, BLOCK, COST, CUT>(p, w, 0);
     }
@@ -92,6 +105,14 @@ struct Share {
     int g;               // CTAs that have a share
     int64_t sums[32];
 };
+
+// CTA `cta`'s entries [lo, hi) of `total`, on a grid of which g CTAs have some.
+__host__ __device__ __forceinline__ void share_of(int64_t total, int grid, int cta, int *g, int64_t *lo, int64_t *hi)
+{
+    *g = total < grid ? static_cast<int>(total) : grid;
+    *lo = cta < *g ? quotient(total * cta, *g) : 0;
+    *hi = cta < *g ? quotient(total * (cta + 1), *g) : 0;
+}
 
 // Every thread of the block calls this (THREADS of them, a multiple of 32).
 // With up to THREADS requests each thread looks at one, once.
@@ -131,14 +152,15 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
         scan(more, &rest);
         total += rest;
     }
-    const int64_t g = total < gridDim.x ? total : static_cast<int64_t>(gridDim.x);
-    const bool mine = blockIdx.x < g;
-    const int64_t lo = mine ? quotient(total * blockIdx.x, g) : 0, hi = mine ? quotient(total * (blockIdx.x + 1), g) : 0;
+    int g;
+    int64_t lo, hi;
+    share_of(total, gridDim.x, blockIdx.x, &g, &lo, &hi);
+    const bool mine = lo < hi;
     if (tid == 0) {
         sh->lo = lo;
         sh->hi = hi;
         sh->total = total;
-        sh->g = static_cast<int>(g);
+        sh->g = g;
     }
     int64_t before = chunk0;
     for (int64_t r = tid;;) {
@@ -159,7 +181,7 @@ __device__ __forceinline__ void find_share(const AttnParams &p, Share *sh)
 }
 
 // The CTA of g whose share holds entry e of the list's `total`.
-__device__ __forceinline__ int owner_of(int64_t e, int g, int64_t total)
+__host__ __device__ __forceinline__ int owner_of(int64_t e, int g, int64_t total)
 {
     return static_cast<int>(quotient((e + 1) * g - 1, total));
 }
@@ -181,10 +203,11 @@ struct Segment {
 template <int ROWS, int BLOCK, int COST, bool CUT>
 struct SegmentWalk {
     int64_t at, hi, total;
-    int g;
+    int g, cta;
     Segment u;            // the unit that `at` falls into
-    __device__ __forceinline__ void begin(const AttnParams &p, const Share &sh)
+    __host__ __device__ __forceinline__ void begin(const AttnParams &p, const Share &sh, int cta_)
     {
+        cta = cta_;
         at = sh.lo;
         hi = sh.hi;
         total = sh.total;
@@ -203,7 +226,7 @@ struct SegmentWalk {
         while (at >= u.unit_first + u.entries) step(p);
     }
     // To the unit that follows.
-    __device__ __forceinline__ void step(const AttnParams &p)
+    __host__ __device__ __forceinline__ void step(const AttnParams &p)
     {
         u.unit_first += u.entries;
         if (++u.tile == u.w.tiles) {
@@ -216,7 +239,7 @@ struct SegmentWalk {
         }
         u.entries = unit_entries<ROWS, BLOCK, COST, CUT>(p, u.w, u.tile);
     }
-    __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
+    __host__ __device__ __forceinline__ bool next(const AttnParams &p, Segment &s)
     {
         while (at < hi) {
             if (at >= u.unit_first + u.entries) step(p);
@@ -229,7 +252,7 @@ struct SegmentWalk {
             s.nb = to - s.b0;
             s.whole = s.nb == u.entries - COST;
             s.parts = 0;
-            if (!s.whole && s.b0 == 0) s.parts = owner_of(unit_end - 1, g, total) - static_cast<int>(blockIdx.x) + 1;
+            if (!s.whole && s.b0 == 0) s.parts = owner_of(unit_end - 1, g, total) - cta + 1;
             return true;
         }
         return false;
@@ -238,7 +261,7 @@ struct SegmentWalk {
 
 // Which of the 32 places j0 .. j0 + 31 a row's token sees, as bits.  node: its
 // index among the request's `nodes` new tokens; tree_row its mask, or NULL.
-__device__ __forceinline__ uint32_t seen_places(const int32_t *tree_row, int tree_words, int node, int nodes,
+__host__ __device__ __forceinline__ uint32_t seen_places(const int32_t *tree_row, int tree_words, int node, int nodes,
                                                 int64_t len, int64_t j0)
 {
     const int64_t ctx = len - nodes;
@@ -257,7 +280,7 @@ __device__ __forceinline__ uint32_t seen_places(const int32_t *tree_row, int tre
         const int64_t w = lo >> 5;
         const uint32_t a = w < tree_words ? static_cast<uint32_t>(tree_row[w]) : 0u;
         const uint32_t b = w + 1 < tree_words ? static_cast<uint32_t>(tree_row[w + 1]) : 0u;
-        m = __funnelshift_r(a, b, static_cast<uint32_t>(lo & 31));
+        m = static_cast<uint32_t>((static_cast<uint64_t>(b) << 32 | a) >> (lo & 31));
     }
     return m & there;
 }

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
     find_share<kRows, kBlock, kCost, false, kThreads>(p, &sh);
 
     SegmentWalk<kRows, kBlock, kCost, false> walk;
-    walk.begin(p, sh);
+    walk.begin(p, sh, static_cast<int>(blockIdx.x));
     Segment seg;
     // The ring: the slot that is consumed next and its phase; requests refill
     // the slot just consumed.

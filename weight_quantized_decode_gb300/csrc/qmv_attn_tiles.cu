@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         const Segment &seg = at.seg;
         uint32_t entry = 0;
         bool ok = true;
-        if (wt == 0) at.walk.begin(p, sh.share);
+        if (wt == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         while (true) {
             group_sync(2, 128);
             if (wt == 0) at.more = at.walk.next(p, at.seg) ? 1 : 0;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         // ---------------- copies: one lane to each box ----------------
         Where &at = sh.where[3];
         const Segment &seg = at.seg;
-        if (lane == 0) at.walk.begin(p, sh.share);
+        if (lane == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         const int page = 1 << p.page_shift;
         const int box_rows = page < kBlock ? page : kBlock;
         const int chunks = kBlock / box_rows;      // of a block: 1 .. 8
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         const uint32_t s_at = tmem + 128 * x, o_at = tmem + 256 + D * x;
         Where &at = sh.where[1 + x];
         const Segment &seg = at.seg;
-        if (lane == 0) at.walk.begin(p, sh.share);
+        if (lane == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         uint32_t entry = 0, segs = 0, np = 0, commits = 0;   // np: phase of this stream's blocks
         bool ok = true;
         while (ok && at.next_for_warp(p)) {
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         Where &at = sh.where[0];
         const Segment &seg = at.seg;
         bool left_unit = false;                    // word of a shared unit left for the second kernel
-        if (tid == 0) at.walk.begin(p, sh.share);
+        if (tid == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         while (true) {
             if (tid == 0) at.more = at.walk.next(p, at.seg) ? 1 : 0;
             group_sync(1, 256);
