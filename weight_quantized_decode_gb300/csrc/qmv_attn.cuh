@@ -314,6 +314,31 @@ __device__ __forceinline__ bool warp_wait_or_give_up(uint64_t *bar, uint32_t par
     return ok;
 }
 
+// Shared-memory accesses by 32-bit address: through a pointer whose memory the
+// compiler cannot tell they would be generic ones, and several times as slow.
+__device__ __forceinline__ float lds1(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t at)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds4u(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts4u(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 2^x (the hardware's approximation; 2^-inf = 0).
 __device__ __forceinline__ float exp2_fast(float x)
 {

@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
     uint8_t *ring = smem + warp * R::kSlots * R::kDataBytes;
     const uint32_t ring_at = smem_u32(ring);
     float *scales = reinterpret_cast<float *>(smem + R::kScaleAt) + warp * R::kSlots * kStep;
+    const uint32_t scales_at = smem_u32(scales);
     __half *pscr = reinterpret_cast<__half *>(smem + R::kPAt) + warp * 8 * 34;
     uint8_t *qbuf = smem + R::kQAt;
     float *oscr = reinterpret_cast<float *>(smem);
@@ -408,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             for (int pm = 0; pm < 2; ++pm) {
                 float d0 = p.scale_log2, d1 = p.scale_log2;
                 if constexpr (KIND == kKvQ8) {
-                    d0 *= scales[slot * kStep + 16 * pm + g];
-                    d1 *= scales[slot * kStep + 16 * pm + 8 + g];
+                    d0 *= lds1(scales_at + 4 * (slot * kStep + 16 * pm + g));
+                    d1 *= lds1(scales_at + 4 * (slot * kStep + 16 * pm + 8 + g));
                 }
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             const uint32_t vb = wait_entry();
             float vfix = 1.0f, vunit = 1.0f;
             if constexpr (KIND == kKvQ8) {
-                float mine = scales[slot * kStep + lane];
+                float mine = lds1(scales_at + 4 * (slot * kStep + lane));
                 if (masked && j0 + lane >= len) mine = 0.0f;
                 const uint32_t bits = __float_as_uint(mine) & 0x7fffffffu;
                 // largest finite scale of the step; a non-finite one makes its own weights non-finite
@@ -504,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             if constexpr (KIND == kKvQ8) {
 #pragma unroll
                 for (int pm = 0; pm < 2; ++pm) {
-                    const float d0 = scales[slot * kStep + 16 * pm + g] * vunit;
-                    const float d1 = scales[slot * kStep + 16 * pm + 8 + g] * vunit;
+                    const float d0 = lds1(scales_at + 4 * (slot * kStep + 16 * pm + g)) * vunit;
+                    const float d1 = lds1(scales_at + 4 * (slot * kStep + 16 * pm + 8 + g)) * vunit;
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         sc[n][pm][0] *= d0;

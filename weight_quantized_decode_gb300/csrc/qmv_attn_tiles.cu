@@ -364,21 +364,21 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                     if (k == 0 ? i < lag : i >= nb) continue;
                     const uint32_t r = entry % R::kRaw, slot = entry % R::kSlots;
                     ok = ok && warp_wait_or_give_up(&b.raw_full[r], (entry / R::kRaw) & 1u, gave_up, p.status);
-                    const uint8_t *raw = smem + R::kRawAt + r * R::kRawBytes;
+                    const uint32_t raw = smem_u32(smem + R::kRawAt) + r * R::kRawBytes;
                     if (ok && k == 1) {
                         // this block's scales, fit for use: none past the end, finite ones
                         // beside a list of the others
                         const uint32_t kept = (first_block + static_cast<uint32_t>(i)) % R::kScales;
-                        const float *src = reinterpret_cast<const float *>(raw + R::kCodeBytes);
-                        float *dst = reinterpret_cast<float *>(smem + R::kScaleAt) + kept * 2 * kBlock;
+                        const uint32_t src = raw + R::kCodeBytes + 4 * wt;
+                        const uint32_t dst = smem_u32(smem + R::kScaleAt) + kept * (2 * kBlock * 4) + 4 * wt;
                         const bool there = (b0 + i) * kBlock + wt < len;
-                        const float kd = src[wt], vd = src[kBlock + wt];
+                        const float kd = lds1(src), vd = lds1(src + 4 * kBlock);
                         const bool finite = (__float_as_uint(vd) & 0x7f800000u) != 0x7f800000u;
                         const float clean = there && finite ? vd : 0.0f;
                         const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(clean) & 0x7fffffffu);
                         const uint32_t odd = __ballot_sync(0xffffffffu, there && !finite);
-                        dst[wt] = kd;
-                        dst[kBlock + wt] = clean;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(kd) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * kBlock), "f"(clean) : "memory");
                         if (lane == 0) {
                             const int e = static_cast<int>(most >> 23) - 126;
                             sh.exponent[kept][warp & 3] = e > 120 ? 120 : e;
@@ -390,12 +390,11 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                     ok = ok && warp_wait_or_give_up(&b.kv_empty[slot], ((entry / R::kSlots) & 1u) ^ 1u, gave_up, p.status);
                     if (!ok) break;
                     // All of the row's codes first: no load can move above a store.
-                    uint8_t *dst = ring + slot * R::kTileBytes + wt * 128;
+                    const uint32_t dst = smem_u32(ring) + slot * R::kTileBytes + wt * 128;
                     uint4 codes[D / 16];
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c)   // as the copies' swizzle of 128 or 64 bytes has them
-                        codes[c] = *reinterpret_cast<const uint4 *>(
-                            raw + wt * D + ((D == 128 ? c ^ (wt & 7) : c ^ ((wt >> 1) & 3)) << 4));
+                        codes[c] = lds4u(raw + wt * D + ((D == 128 ? c ^ (wt & 7) : c ^ ((wt >> 1) & 3)) << 4));
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
                         const uint4 q = codes[c];
@@ -410,9 +409,9 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                             f[2 * j] = *reinterpret_cast<const uint32_t *>(&lo);
                             f[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&hi);
                         }
-                        uint8_t *half = dst + (c >> 2) * R::kHalfBytes;
-                        *reinterpret_cast<uint4 *>(half + ((((2 * c) & 7) ^ (wt & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-                        *reinterpret_cast<uint4 *>(half + ((((2 * c + 1) & 7) ^ (wt & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+                        const uint32_t half = dst + (c >> 2) * R::kHalfBytes;
+                        sts4u(half + ((((2 * c) & 7) ^ (wt & 7)) << 4), make_uint4(f[0], f[1], f[2], f[3]));
+                        sts4u(half + ((((2 * c + 1) & 7) ^ (wt & 7)) << 4), make_uint4(f[4], f[5], f[6], f[7]));
                     }
                     fence_async();
                     __syncwarp();
@@ -686,13 +685,13 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             for (int i = two ? 0 : x; ok && i < nb; i += two ? 1 : 2, ns ^= 1u) {
                 const int64_t j0 = (b0 + i) * kBlock;
                 const bool masked = j0 + kBlock > open;
-                const float *kd = nullptr, *vd = nullptr;   // 8-bit rows: the block's scales
+                uint32_t kd = 0u, vd = 0u;                  // 8-bit rows: the block's scales, in shared memory
                 float vfix = 1.0f, vunit = 1.0f;
                 if constexpr (KIND == kKvQ8) {
                     const uint32_t block = entry / 2 + static_cast<uint32_t>(i), kept = block % R::kScales;
                     ok = warp_wait_or_give_up(&b.scale_full[kept], (block / R::kScales) & 1u, gave_up, p.status);
-                    kd = reinterpret_cast<const float *>(smem + R::kScaleAt) + kept * 2 * kBlock;
-                    vd = kd + kBlock;
+                    kd = smem_u32(smem + R::kScaleAt) + kept * (2 * kBlock * 4);
+                    vd = kd + kBlock * 4;
                     int e = sh.exponent[kept][0];
 #pragma unroll
                     for (int w = 1; w < 4; ++w) e = sh.exponent[kept][w] > e ? sh.exponent[kept][w] : e;
@@ -723,7 +722,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         if constexpr (KIND == kKvQ8) {
 #pragma unroll
                             for (int k = 0; k < 64; k += 4) {
-                                const float4 d = *reinterpret_cast<const float4 *>(kd + 64 * h + k);
+                                const float4 d = lds4(kd + 256 * h + 4 * k);
                                 const uint64_t a = mul2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), pair(d.x, d.y));
                                 const uint64_t c = mul2(pair(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), pair(d.z, d.w));
                                 s[k] = __float_as_uint(low(a));
@@ -753,19 +752,25 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                             float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                             sum[0] = sum[1] = 0ull;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
-                                const uint64_t e = fma2(pair(s0, s1), scale2, c2);
-                                const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
-                                sum[k & 1] = add2(sum[k & 1], pair(a, c));
-                                if constexpr (KIND == kKvQ8) {
-                                    const float2 d = *reinterpret_cast<const float2 *>(vd + 64 * h + 2 * k);
-                                    const uint64_t g = mul2(pair(a, c), mul2(pair(d.x, d.y), pair(vunit, vunit)));
-                                    w[k] = float2_to_half2_bits(make_float2(low(g), high(g)));
-                                } else {
-                                    w[k] = float2_to_half2_bits(make_float2(a, c));
+                            for (int k2 = 0; k2 < 16; ++k2) {
+                                float4 d = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                                if constexpr (KIND == kKvQ8) d = lds4(vd + 256 * h + 16 * k2);
+#pragma unroll
+                                for (int i2 = 0; i2 < 2; ++i2) {
+                                    const int k = 2 * k2 + i2;
+                                    const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
+                                    const uint64_t e = fma2(pair(s0, s1), scale2, c2);
+                                    const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
+                                    sum[i2] = add2(sum[i2], pair(a, c));
+                                    if constexpr (KIND == kKvQ8) {
+                                        const uint64_t unit = mul2(i2 ? pair(d.z, d.w) : pair(d.x, d.y), pair(vunit, vunit));
+                                        const uint64_t g = mul2(pair(a, c), unit);
+                                        w[k] = float2_to_half2_bits(make_float2(low(g), high(g)));
+                                    } else {
+                                        w[k] = float2_to_half2_bits(make_float2(a, c));
+                                    }
+                                    t[k & 3] = fmaxf(t[k & 3], fmaxf(s0, s1));
                                 }
-                                t[k & 3] = fmaxf(t[k & 3], fmaxf(s0, s1));
                             }
                             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
                             const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
