@@ -19,6 +19,12 @@
 // multiplies the score, the value scale the weight, both in fp32; weights are
 // held below fp16's largest value by a running power of two of the largest
 // value scale, handled like the running maximum.
+//   Measured: 64 requests of 100 to 16383 8-bit places, one token of 32 heads on
+// 8 of 128: 185 us, 6.1 TB/s, 0.90 of the measured copy bandwidth; 16 uneven
+// trees of up to 24 nodes over 511 to 8191 fp16 places, 16 heads on 8: 63 us,
+// 0.68.  One request has little to stream and pays for the start, the ragged
+// end and the join: 8 nodes over 30001 places 35 us where the bytes take 18,
+// one token over 4095 places 9.8 us where they take 2.5.
 #include <cstdint>
 
 #include "qmv_attn.cuh"

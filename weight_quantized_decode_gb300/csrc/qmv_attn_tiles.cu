@@ -10,16 +10,28 @@
 //     of 128 places, so that a block is read once for 256 rows;
 //   * up to 128 rows: both streams hold the same rows, one takes the even and
 //     one the odd blocks, and their outputs are joined at the end of a segment.
-// While one stream's scores go through its softmax, the other's products run.
 //   s = q k^T: queries and keys from shared memory (K-major, 128-byte swizzle,
 // as the tensor copies deliver them).  The weights p go back to tensor memory
 // over the scores they came from, as fp16, and are the A operand of o += p v;
-// values are read N-major from the same kind of tile.  A thread owns a row: its
-// maximum and sum need no exchange.  The output in tensor memory is rescaled
+// values are read N-major from the same kind of tile.  Both go by halves of 64
+// places: as soon as a half's weights are there, their product and that half of
+// the next block's scores are issued, beside the softmax of the other half (by
+// whole blocks a prompt chunk took 190 us, by halves 161).  A thread owns a row:
+// its maximum and sum need no exchange.  The output in tensor memory is rescaled
 // only where a row's maximum has risen by more than 2^5 since it last was; until
 // then the weights simply come out larger, p <= 2^(10 + 5) < 65504.
+//   8-bit rows: a fourth warpgroup expands codes to fp16 tiles (exact integers);
+// scales multiply scores and weights in fp32, weights are held below fp16's
+// largest value by a running power of two.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
-// the copies.  All waits are bounded.
+// the copies, 12-15 expand codes.  All waits are bounded.
+//   What bounds it: up to 128 rows the bytes (16 nodes of 4 heads a group over
+// 262147 places of 128: 170 us, 6.3 TB/s, 0.93 of the measured copy bandwidth);
+// more rows the softmax, whose two warps on each scheduler take some 2900 cycles
+// a block of 256 rows where the products would take 2048 (128 columns; two
+// chunks of 1400 and 1500 tokens behind 2000 and 2800, 32 heads on 8: 161 us,
+// 910 TFLOP/s of useful products, 0.48 of the measured bf16 peak; 64 columns:
+// eight trees of 64 nodes over 4001 to 8001 places, 64 heads on 8: 92 us).
 #include <cstdint>
 
 #include "qmv_attn.cuh"
@@ -721,14 +733,20 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         ld_wait(s + 32);
                         if constexpr (KIND == kKvQ8) {
 #pragma unroll
-                            for (int k = 0; k < 64; k += 4) {
-                                const float4 d = lds4(kd + 256 * h + 4 * k);
-                                const uint64_t a = mul2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), pair(d.x, d.y));
-                                const uint64_t c = mul2(pair(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), pair(d.z, d.w));
-                                s[k] = __float_as_uint(low(a));
-                                s[k + 1] = __float_as_uint(high(a));
-                                s[k + 2] = __float_as_uint(low(c));
-                                s[k + 3] = __float_as_uint(high(c));
+                            for (int g = 0; g < 2; ++g) {
+                                float4 d[8];   // eight loads at a time, then their uses
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) d[i] = lds4(kd + 256 * h + 128 * g + 16 * i);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    uint32_t *v = s + 32 * g + 4 * i;
+                                    const uint64_t lo = mul2(pair(__uint_as_float(v[0]), __uint_as_float(v[1])), pair(d[i].x, d[i].y));
+                                    const uint64_t hi = mul2(pair(__uint_as_float(v[2]), __uint_as_float(v[3])), pair(d[i].z, d[i].w));
+                                    v[0] = __float_as_uint(low(lo));
+                                    v[1] = __float_as_uint(high(lo));
+                                    v[2] = __float_as_uint(low(hi));
+                                    v[3] = __float_as_uint(high(hi));
+                                }
                             }
                         }
                         if (masked) {
@@ -751,10 +769,14 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                             const uint64_t scale2 = pair(scale, scale), c2 = pair(c0, c0);
                             float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                             sum[0] = sum[1] = 0ull;
+                            float4 dv[4];
 #pragma unroll
                             for (int k2 = 0; k2 < 16; ++k2) {
-                                float4 d = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-                                if constexpr (KIND == kKvQ8) d = lds4(vd + 256 * h + 16 * k2);
+                                if constexpr (KIND == kKvQ8) {
+                                    if (k2 % 4 == 0)
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) dv[i] = lds4(vd + 256 * h + 16 * (k2 + i));
+                                }
 #pragma unroll
                                 for (int i2 = 0; i2 < 2; ++i2) {
                                     const int k = 2 * k2 + i2;
@@ -763,6 +785,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                                     const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
                                     sum[i2] = add2(sum[i2], pair(a, c));
                                     if constexpr (KIND == kKvQ8) {
+                                        const float4 d = dv[k2 & 3];
                                         const uint64_t unit = mul2(i2 ? pair(d.z, d.w) : pair(d.x, d.y), pair(vunit, vunit));
                                         const uint64_t g = mul2(pair(a, c), unit);
                                         w[k] = float2_to_half2_bits(make_float2(low(g), high(g)));
