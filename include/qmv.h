@@ -1,8 +1,9 @@
 /*
  * qmv.h -- C ABI of the block-quantised weight x activation product used by
- * single-stream LLM decode, for one NVIDIA GB300 (sm_103a).
+ * single-stream LLM decode, and of the paged key/value cache and attention
+ * that stand between two such products, for one NVIDIA GB300 (sm_103a).
  *
- * The operation, for every call below (one token's decode step multiplies its
+ * The operation, for every product below (one token's decode step multiplies its
  * activation row by each weight matrix in turn -- H100-KERNEL-5X-ROADMAP,
  * "Why the decode gap is bandwidth, not arithmetic"):
  *

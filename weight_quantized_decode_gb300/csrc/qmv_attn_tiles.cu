@@ -492,11 +492,13 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 const int64_t j = (b0 + i) * kBlock + c * box_rows;
                 const int y = y_head + (static_cast<int>(j & (page - 1)) & ~(box_rows - 1));
                 const CUtensorMap *map = values ? &vmap : &kmap;
+                // (test only) the first tile of CTA 0 is expected but never requested
+                const bool skip = p.test_skip_copy && blockIdx.x == 0 && entry == 0u;
                 if constexpr (KIND == kKvF16) {
-                    if (h < R::kHalves && id >= 0)
+                    if (h < R::kHalves && id >= 0 && !skip)
                         copy_box(dst + h * R::kHalfBytes + c * box_rows * 128, map, 64 * h, y, id, full);
                 } else {
-                    if (h == 0 && id >= 0) copy_box(dst + c * box_rows * D, map, 0, y, id, full);
+                    if (h == 0 && id >= 0 && !skip) copy_box(dst + c * box_rows * D, map, 0, y, id, full);
                     if (!values && (h == 1 || h == 2) && id >= 0) {
                         const float *src = (h == 1 ? p.k_scale : p.v_scale) + ((static_cast<int64_t>(id) * p.Hkv) << p.page_shift) + y;
                         bulk_g2s(dst + R::kCodeBytes + (h - 1) * kBlock * 4 + c * box_rows * 4, src, box_rows * 4, full);

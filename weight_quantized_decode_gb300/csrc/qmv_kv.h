@@ -53,6 +53,7 @@ struct AttnParams {
     int Hq, Hkv, group, tree_words, page_shift;
     float scale_log2;            // softmax scale times log2(e)
     int *status;
+    int test_skip_copy;          // failure-detection test only: CTA 0 never requests its first keys
 };
 
 cudaError_t launch_kv_pages(const PagesParams &p, int sms, cudaStream_t s, bool pdl);

@@ -1,7 +1,10 @@
 // qmv_kv_api.cu -- C entry points of the paged-cache calls (include/qmv.h):
 // argument validation and the hand-over to the launchers.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 
 #include "../../include/qmv.h"
 #include "qmv_kv.h"
@@ -32,6 +35,21 @@ qmv_status check_cache(int64_t n_pages, int64_t Hkv, int64_t page, int64_t D, in
     // 16-byte rows of every page: the strides the copies need
     if ((page_stride * (kind == QMV_KV_F16 ? 2 : 1)) % 16 != 0) return QMV_ERR_ALIGN;
     return QMV_OK;
+}
+
+// Failure detection is tested without a GPU fault: QMV_TEST_SKIP_COPY="attn:N"
+// makes the N-th attention launch (counted from 1) of this process skip a copy
+// whose bytes a barrier still expects.  The waits on it run out, the kernel
+// records QMV_DEV_TIMEOUT, gives that CTA's outputs as NaN and returns.  Unset
+// in every normal run.
+bool test_skip_this_launch()
+{
+    static const long long armed = [] {
+        const char *e = std::getenv("QMV_TEST_SKIP_COPY");
+        return e && !std::strncmp(e, "attn:", 5) ? std::atoll(e + 5) : 0ll;
+    }();
+    static std::atomic<long long> seen{0};
+    return armed > 0 && seen.fetch_add(1) + 1 == armed;
 }
 
 }  // namespace
@@ -206,6 +224,7 @@ qmv_status qmv_tree_attn(const void *q, int64_t q_stride, const void *k, const v
     p.group = static_cast<int>(Hq / Hkv);
     p.tree_words = static_cast<int>(tree_words);
     p.page_shift = page_shift_of(page);
+    p.test_skip_copy = test_skip_this_launch() ? 1 : 0;
     p.scale_log2 = (scale ? *scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
     if (launch_tree_attn(p, static_cast<int>(D), kind, sms, reinterpret_cast<cudaStream_t>(stream), pdl) !=
         cudaSuccess) {
