@@ -108,3 +108,19 @@ def test_calls_on_several_streams(q):
 def test_a_workspace_is_made_where_none_is_given(q):
     prob = ref.problem([700], [3], 8, 2, 64, 16, seed=8)
     check(q, prob, None)
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.3, -0.3, 1.0])
+@pytest.mark.parametrize("heads,D,T", [(4, 64, 6), (4, 128, 3), (16, 64, 20), (16, 128, 40)])
+def test_row_scales_of_either_sign_and_zero(q, ws, heads, D, T, scale):
+    """8-bit rows whose scales are negative, zero (over codes that are not),
+    least normal or subnormal: hidden places stay hidden, the others count."""
+    prob = ref.problem([70, 3], [T, 5], heads, 2, D, 16, q8=True, tree="random", seed=T)
+    rs = np.random.RandomState(1)
+    for name in ("k_scale", "v_scale"):
+        arr = prob[name]
+        arr *= np.where(rs.rand(*arr.shape) < 0.4, -1.0, 1.0).astype(np.float32)
+        for value in (0.0, -0.0, 2.0 ** -126, 2.0 ** -149):
+            arr[rs.rand(*arr.shape) < 0.06] = value
+    check(q, prob, ws, scale=scale)
+    check(q, {**prob, "tree": None}, ws, scale=scale)

@@ -22,7 +22,9 @@
 // then the weights simply come out larger, p <= 2^(10 + 5) < 65504.
 //   8-bit rows: a fourth warpgroup expands codes to fp16 tiles (exact integers);
 // scales multiply scores and weights in fp32, weights are held below fp16's
-// largest value by a running power of two.
+// largest value by a running power of two, which enters through the exponent.
+// The scales' arithmetic makes the softmax longer still: the chunks and the eight
+// trees of the figures below take 247 and 147 us, the 16 nodes 198.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
 // the copies, 12-15 expand codes.  All waits are bounded.
 //   What bounds it: up to 128 rows the bytes (16 nodes of 4 heads a group over
@@ -260,9 +262,11 @@ struct Shared {
     Where where[5];           // the softmax groups, the streams' products, the copies, the expanding warps
     float m[kTile], l[kTile];
     int ve;
-    // 8-bit rows, of each block kept: by 32 places, which value scales are not
-    // finite, and the exponent above the largest of the others
+    // 8-bit rows, of each block kept: by 32 places, whose scales are not finite,
+    // whose key scales are negative, and the exponent above the largest of the
+    // finite value scales
     uint32_t odd[16][4];
+    uint32_t below[16][4];
     int exponent[16][4];
 };
 
@@ -356,6 +360,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kExpandRegs));
         // ---------------- codes to fp16 tiles: a thread to a row ----------------
         const int wt = tid & 127;
+        const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);   // as the softmax groups have it
         Where &at = sh.where[4];
         const Segment &seg = at.seg;
         uint32_t entry = 0;
@@ -378,23 +383,35 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                     ok = ok && warp_wait_or_give_up(&b.raw_full[r], (entry / R::kRaw) & 1u, gave_up, p.status);
                     const uint32_t raw = smem_u32(smem + R::kRawAt) + r * R::kRawBytes;
                     if (ok && k == 1) {
-                        // this block's scales, fit for use: none past the end, finite ones
-                        // beside a list of the others
+                        // This block's scales, fit for use.  Keys: times the softmax scale.
+                        // Values: over a power of two to 32 places, which goes into the
+                        // exponent of the weights.  Ones that are not finite are listed and
+                        // replaced, so that they reach no row that does not see them.  The
+                        // -inf of a place that a row does not see has to survive its key scale:
+                        // one of 0 becomes the least normal number, whose scores are below
+                        // 2^-90 and so 0 beside any other, and negative ones are listed.
                         const uint32_t kept = (first_block + static_cast<uint32_t>(i)) % R::kScales;
                         const uint32_t src = raw + R::kCodeBytes + 4 * wt;
                         const uint32_t dst = smem_u32(smem + R::kScaleAt) + kept * (2 * kBlock * 4) + 4 * wt;
                         const bool there = (b0 + i) * kBlock + wt < len;
-                        const float kd = lds1(src), vd = lds1(src + 4 * kBlock);
-                        const bool finite = (__float_as_uint(vd) & 0x7f800000u) != 0x7f800000u;
-                        const float clean = there && finite ? vd : 0.0f;
-                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(clean) & 0x7fffffffu);
-                        const uint32_t odd = __ballot_sync(0xffffffffu, there && !finite);
+                        float kd = lds1(src), vd = lds1(src + 4 * kBlock);
+                        const bool k_finite = (__float_as_uint(kd) & 0x7f800000u) != 0x7f800000u;
+                        const bool v_finite = (__float_as_uint(vd) & 0x7f800000u) != 0x7f800000u;
+                        kd = fminf(fmaxf(kd * scale, -3.402823466e38f), 3.402823466e38f);
+                        if (kd == 0.0f) kd = 1.175494351e-38f;
+                        if (!there || !k_finite) kd = 1.0f;
+                        if (!there || !v_finite) vd = 0.0f;
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(vd) & 0x7fffffffu);
+                        const uint32_t odd = __ballot_sync(0xffffffffu, there && !(k_finite && v_finite));
+                        const uint32_t below = __ballot_sync(0xffffffffu, kd < 0.0f);
+                        int e = static_cast<int>(most >> 23) - 126;
+                        e = e > 120 ? 120 : e;
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(kd) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * kBlock), "f"(clean) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * kBlock), "f"(vd * power_of_2(-e)) : "memory");
                         if (lane == 0) {
-                            const int e = static_cast<int>(most >> 23) - 126;
-                            sh.exponent[kept][warp & 3] = e > 120 ? 120 : e;
+                            sh.exponent[kept][warp & 3] = e;
                             sh.odd[kept][warp & 3] = odd;
+                            sh.below[kept][warp & 3] = below;
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&b.scale_full[kept]);
@@ -700,21 +717,22 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 const int64_t j0 = (b0 + i) * kBlock;
                 const bool masked = j0 + kBlock > open;
                 uint32_t kd = 0u, vd = 0u;                  // 8-bit rows: the block's scales, in shared memory
-                float vfix = 1.0f, vunit = 1.0f;
+                float vfix = 1.0f;
+                const int *ev = nullptr;                    // and the exponents of its value scales
                 if constexpr (KIND == kKvQ8) {
                     const uint32_t block = entry / 2 + static_cast<uint32_t>(i), kept = block % R::kScales;
                     ok = warp_wait_or_give_up(&b.scale_full[kept], (block / R::kScales) & 1u, gave_up, p.status);
                     kd = smem_u32(smem + R::kScaleAt) + kept * (2 * kBlock * 4);
                     vd = kd + kBlock * 4;
-                    int e = sh.exponent[kept][0];
+                    ev = sh.exponent[kept];
+                    int e = ev[0];
 #pragma unroll
-                    for (int w = 1; w < 4; ++w) e = sh.exponent[kept][w] > e ? sh.exponent[kept][w] : e;
+                    for (int w = 1; w < 4; ++w) e = ev[w] > e ? ev[w] : e;
                     if (e > ve) {
                         vfix = exp2_fast(static_cast<float>(ve - e));
                         ve = e;
                     }
-                    vunit = power_of_2(-ve);
-                    // a value scale that is not finite makes the rows that see it NaN
+                    // a scale that is not finite makes the rows that see its place NaN
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t odd = sh.odd[kept][w];
@@ -733,71 +751,76 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         ld_32cols(s_at + 64 * h + 32, s + 32);
                         ld_wait(s);
                         ld_wait(s + 32);
-                        if constexpr (KIND == kKvQ8) {
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                float4 d[8];   // eight loads at a time, then their uses
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) d[i] = lds4(kd + 256 * h + 128 * g + 16 * i);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    uint32_t *v = s + 32 * g + 4 * i;
-                                    const uint64_t lo = mul2(pair(__uint_as_float(v[0]), __uint_as_float(v[1])), pair(d[i].x, d[i].y));
-                                    const uint64_t hi = mul2(pair(__uint_as_float(v[2]), __uint_as_float(v[3])), pair(d[i].z, d[i].w));
-                                    v[0] = __float_as_uint(low(lo));
-                                    v[1] = __float_as_uint(high(lo));
-                                    v[2] = __float_as_uint(low(hi));
-                                    v[3] = __float_as_uint(high(hi));
-                                }
-                            }
-                        }
                         if (masked) {
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 const uint32_t see =
                                     seen_places(tree_row, p.tree_words, node, seg.w.nodes, len, j0 + 64 * h + 32 * c);
+                                const uint32_t kept = (entry / 2 + static_cast<uint32_t>(i)) % R::kScales;
+                                const uint32_t below = KIND == kKvQ8 ? sh.below[kept][2 * h + c] : 0u;
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u;   // -inf
+                                for (int k = 0; k < 32; ++k)   // -inf, once the scale has multiplied it
+                                    if (!(see >> k & 1u)) s[32 * c + k] = 0xff800000u ^ (below >> k & 1u) << 31;
                             }
                         }
                         uint32_t w[32];
-                        uint64_t sum[2];
+                        float l_half;
                         // Weights by the maximum so far, beside the maximum of these
                         // scores; where one lies past the lag, the outputs follow the new
                         // maximum and the weights are taken again.
                         while (true) {
                             const float c0 = kShift - (m == -INFINITY ? 0.0f : m);
-                            const uint64_t scale2 = pair(scale, scale), c2 = pair(c0, c0);
-                            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                            sum[0] = sum[1] = 0ull;
-                            float4 dv[4];
+                            float top;
+                            if constexpr (KIND == kKvF16) {
+                                const uint64_t scale2 = pair(scale, scale), c2 = pair(c0, c0);
+                                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                                uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                            for (int k2 = 0; k2 < 16; ++k2) {
-                                if constexpr (KIND == kKvQ8) {
-                                    if (k2 % 4 == 0)
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) dv[i] = lds4(vd + 256 * h + 16 * (k2 + i));
-                                }
-#pragma unroll
-                                for (int i2 = 0; i2 < 2; ++i2) {
-                                    const int k = 2 * k2 + i2;
+                                for (int k = 0; k < 32; ++k) {
                                     const float s0 = __uint_as_float(s[2 * k]), s1 = __uint_as_float(s[2 * k + 1]);
                                     const uint64_t e = fma2(pair(s0, s1), scale2, c2);
                                     const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
-                                    sum[i2] = add2(sum[i2], pair(a, c));
-                                    if constexpr (KIND == kKvQ8) {
-                                        const float4 d = dv[k2 & 3];
-                                        const uint64_t unit = mul2(i2 ? pair(d.z, d.w) : pair(d.x, d.y), pair(vunit, vunit));
-                                        const uint64_t g = mul2(pair(a, c), unit);
-                                        w[k] = float2_to_half2_bits(make_float2(low(g), high(g)));
-                                    } else {
-                                        w[k] = float2_to_half2_bits(make_float2(a, c));
-                                    }
+                                    sum[k & 1] = add2(sum[k & 1], pair(a, c));
+                                    w[k] = float2_to_half2_bits(make_float2(a, c));
                                     t[k & 3] = fmaxf(t[k & 3], fmaxf(s0, s1));
                                 }
+                                sum[0] = add2(sum[0], sum[1]);
+                                l_half = low(sum[0]) + high(sum[0]);
+                                top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
+                            } else {
+                                // Weights carry their 32 places' power of two, 2^(e - ve), in the
+                                // exponent (not below 2^-40: such values are lost in the others'
+                                // rounding), and the sum is taken without it.
+                                l_half = 0.0f;
+                                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                                for (int g = 0; g < 2; ++g) {
+                                    const int drop = ev[2 * h + g] - ve;
+                                    const float by = drop < -40 ? -40.0f : static_cast<float>(drop);
+                                    const uint64_t c2 = pair(c0 + by, c0 + by);
+                                    float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                                    for (int k4 = 0; k4 < 8; ++k4) {
+                                        const float4 d = lds4(kd + 256 * h + 128 * g + 16 * k4), dv = lds4(vd + 256 * h + 128 * g + 16 * k4);
+#pragma unroll
+                                        for (int i2 = 0; i2 < 2; ++i2) {
+                                            const int k = 16 * g + 2 * k4 + i2;
+                                            const uint64_t e = fma2(pair(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])),
+                                                                    i2 ? pair(d.z, d.w) : pair(d.x, d.y), c2);
+                                            const float a = exp2_fast(low(e)), c = exp2_fast(high(e));
+                                            sum[i2] = add2(sum[i2], pair(a, c));
+                                            const uint64_t q = mul2(pair(a, c), i2 ? pair(dv.z, dv.w) : pair(dv.x, dv.y));
+                                            w[k] = float2_to_half2_bits(make_float2(low(q), high(q)));
+                                            u[k & 3] = fmaxf(u[k & 3], fmaxf(low(e), high(e)));
+                                        }
+                                    }
+                                    sum[0] = add2(sum[0], sum[1]);
+                                    l_half += (low(sum[0]) + high(sum[0])) * exp2_fast(-by);
+                                    t[g] = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) - (c0 + by);
+                                }
+                                top = fmaxf(t[0], t[1]);
                             }
-                            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
                             const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
                             if (!__any_sync(0xffffffffu, rises) && vfix == 1.0f) break;
                             if (!first) {
@@ -823,8 +846,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         }
                         if (!ok) break;
                         st_32cols(s_at + 64 * h, w);
-                        sum[0] = add2(sum[0], sum[1]);
-                        l += low(sum[0]) + high(sum[0]);
+                        l += l_half;
                     }
                     if (KIND == kKvF16 && masked && (wt >> 6) == h && j0 + wt >= ctx) {
                         // Value rows past the end are cleared, and so are nodes' rows
