@@ -267,3 +267,24 @@ def test_refusals(q):
     with pytest.raises(TypeError):
         q.KvCache(c.k.float(), c.v.float())
     assert q.qmv_device_status() == 0
+
+
+def test_cache_objects_cannot_be_changed_and_follow_their_storage(q):
+    """A KvCache refuses other tensors; its calls use its tensors' memory as it
+    is at the call, also after the storage was given up and taken again."""
+    c = q.qmv_kv_cache(4, 2, 16, 64)
+    for name in ("k", "kind", "page_stride"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+    qkv = torch.randn(3, (4 + 2 * 2) * 64, device="cuda")
+    slots = torch.tensor([0, 17, 63], dtype=torch.int32, device="cuda")
+    size, old = c.k.untyped_storage().nbytes(), c.k.data_ptr()
+    c.k.untyped_storage().resize_(0)
+    keep = torch.empty(size, dtype=torch.uint8, device="cuda")     # takes the old place
+    c.k.untyped_storage().resize_(size)
+    keep.zero_()
+    q.qmv_kv_append(qkv, c, slots, 4)
+    at = [(int(s) // 16, int(s) % 16) for s in slots]
+    for t, (page, row) in enumerate(at):
+        assert torch.equal(c.k[page, :, row], qkv[t, 256:384].half().view(2, 64))
+    assert c.k.data_ptr() == old or not keep.any()

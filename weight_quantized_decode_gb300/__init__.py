@@ -478,9 +478,11 @@ def qmv_device_status(stream=None) -> int:
 class KvCache:
     """A paged key/value cache: k and v [n_pages, kv_heads, page, head_dim], fp16 or int8 (then with one fp32
     scale to a row, k_scale and v_scale [n_pages, kv_heads, page]).  The rows of a page are dense; pages may lie
-    apart by any stride the two share (k and v interleaved in one buffer, for instance)."""
+    apart by any stride the two share (k and v interleaved in one buffer, for instance).  What the object says of its
+    tensors is checked once, here: it cannot be given others (make another KvCache, which is cheap)."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads", "page", "head_dim", "kind", "device", "index", "_args")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads", "page", "head_dim", "kind", "device", "index",
+                 "page_stride")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         torch = _torch()
@@ -494,19 +496,26 @@ class KvCache:
         dense = (page * dim, dim, 1)
         if tuple(k.stride()[1:]) != dense or tuple(v.stride()[1:]) != dense or (n_pages > 1 and k.stride(0) != v.stride(0)):
             raise ValueError("KvCache: the rows of a page must be dense, and k and v have one page stride")
-        self.kind = QMV_KV_F16 if k.dtype == torch.float16 else QMV_KV_Q8
+        kind = QMV_KV_F16 if k.dtype == torch.float16 else QMV_KV_Q8
         for s in (k_scale, v_scale):
-            if (self.kind == QMV_KV_Q8) != (s is not None):
+            if (kind == QMV_KV_Q8) != (s is not None):
                 raise ValueError("KvCache: an int8 cache has k_scale and v_scale, a float16 cache has none")
             if s is not None and not (s.is_cuda and s.device == k.device and s.dtype == torch.float32
                                       and s.is_contiguous() and tuple(s.shape) == (n_pages, heads, page)):
                 raise ValueError("KvCache: scales must be contiguous float32 [n_pages, kv_heads, page] beside k and v")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.kv_heads, self.page, self.head_dim = n_pages, heads, page, dim
-        self.device, self.index = k.device, k.get_device()
-        stride = k.stride(0) if n_pages > 1 else heads * page * dim
-        self._args = (k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else 0,
-                      v_scale.data_ptr() if v_scale is not None else 0, stride)
+        values = (k, v, k_scale, v_scale, n_pages, heads, page, dim, kind, k.device, k.get_device(),
+                  k.stride(0) if n_pages > 1 else heads * page * dim)
+        for name, value in zip(self.__slots__, values):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"KvCache: {name} cannot be set")
+
+    def _ptrs(self):
+        """Addresses of k, v and the scales, as they are now."""
+        if self.kind == QMV_KV_F16:
+            return self.k.data_ptr(), self.v.data_ptr(), 0, 0
+        return self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr()
 
 
 def qmv_kv_cache(n_pages, kv_heads, page, head_dim, dtype=None, device="cuda"):
@@ -641,11 +650,11 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
         q = torch.empty((T, n_heads, D), dtype=torch.float16, device=cache.device)
     elif not (q.get_device() == at and q.dtype is torch.float16 and q.is_contiguous() and q.numel() == T * n_heads * D):
         raise ValueError(f"{fn}: q must be a contiguous CUDA float16 tensor of {T}x{n_heads}x{D}")
-    k, v, ks, vs, page_stride = cache._args
+    k, v, ks, vs = cache._ptrs()
     _call_on(fn, at, stream,
              (qkv.data_ptr(), apart[0] if T > 1 else wide, f32, slots_ptr, pos_ptr, cos_ptr, sin_ptr, n_pos, rot,
               bool(interleaved), q.data_ptr(), k, v, ks, vs, cache.kind, T, int(n_heads), hk, D, cache.n_pages,
-              cache.page, page_stride))
+              cache.page, cache.page_stride))
     return q
 
 
@@ -693,10 +702,10 @@ def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=Non
         workspace = qmv_tree_attn_workspace(cache.device)
     elif workspace.get_device() != at or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
-    k, v, ks, vs, page_stride = cache._args
+    k, v, ks, vs = cache._ptrs()
     _call_on(fn, at, stream,
              (q.data_ptr(), apart[0] if T > 1 else H * D, k, v, ks, vs, cache.kind, cache.n_pages, cache.page,
-              page_stride, table_ptr, width, start_ptr, len_ptr, tree_ptr, words,
+              cache.page_stride, table_ptr, width, start_ptr, len_ptr, tree_ptr, words,
               None if scale is None else ctypes.byref(ctypes.c_float(scale)), out.data_ptr(), workspace.data_ptr(),
               workspace.nbytes, R, T, H, cache.kv_heads, D))
     return out
