@@ -16,7 +16,7 @@
 // values are read N-major from the same kind of tile.  Both go by halves of 64
 // places: as soon as a half's weights are there, their product and that half of
 // the next block's scores are issued, beside the softmax of the other half (by
-// whole blocks a prompt chunk took 190 us, by halves 161).  A thread owns a row:
+// whole blocks two prompt chunks took 190 us, by halves 161).  A thread owns a row:
 // its maximum and sum need no exchange.  The output in tensor memory is rescaled
 // only where a row's maximum has risen by more than 2^5 since it last was; until
 // then the weights simply come out larger, p <= 2^(10 + 5) < 65504.
@@ -24,16 +24,24 @@
 // scales multiply scores and weights in fp32, weights are held below fp16's
 // largest value by a running power of two, which enters through the exponent.
 // The scales' arithmetic makes the softmax longer still: the chunks and the eight
-// trees of the figures below take 247 and 147 us, the 16 nodes 198.
+// trees of the figures below take 248 and 145 us, the 16 nodes 201.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
-// the copies, 12-15 expand codes.  All waits are bounded.
+// the copies, 11 brings the next segment's queries as soon as the last products
+// have read this one's (loaded by the softmax groups at a segment's start instead,
+// the two prompt chunks took 161 us, not 151), 12-15 expand codes.  All waits are
+// bounded.
 //   What bounds it: up to 128 rows the bytes (16 nodes of 4 heads a group over
-// 262147 places of 128: 170 us, 6.3 TB/s, 0.93 of the measured copy bandwidth);
-// more rows the softmax, whose two warps on each scheduler take some 2900 cycles
-// a block of 256 rows where the products would take 2048 (128 columns; two
-// chunks of 1400 and 1500 tokens behind 2000 and 2800, 32 heads on 8: 161 us,
-// 910 TFLOP/s of useful products, 0.48 of the measured bf16 peak; 64 columns:
-// eight trees of 64 nodes over 4001 to 8001 places, 64 heads on 8: 92 us).
+// 262147 places of 128: 172 us, 6.2 TB/s, 0.92 of the measured copy bandwidth);
+// more rows the softmax: each half of a block is a chain of some 1700 cycles for
+// its warp (about 850 of arithmetic, the rest waiting for scores to arrive from
+// and weights to arrive in tensor memory), two warps share a scheduler, and the
+// products, 2048 cycles a block of 256 rows at 128 columns, pass beside it (two
+// chunks of 1400 and 1500 tokens behind 2000 and 2800, 32 heads on 8: 151 us,
+// 970 TFLOP/s of useful products, 0.51 of the measured bf16 peak; 64 columns:
+// eight trees of 64 nodes over 4001 to 8001 places, 64 heads on 8: 91 us).  A
+// share of the exponentials as polynomials in place of the special-function unit
+// made it slower (a quarter of them: 105 for 91 us), and so did passing a half's
+// weights on only after asking for the next scores (170 for 155).
 #include <cstdint>
 
 #include "qmv_attn.cuh"
@@ -46,8 +54,9 @@ namespace {
 constexpr int kTile = 128;           // rows of a stream
 constexpr int kRows = 2 * kTile;     // rows of a unit
 constexpr int kBlock = 128;          // places of a block
-constexpr int kCost = 6;             // what a unit costs besides its blocks, in blocks
+constexpr int kCost = 5;             // what a unit costs besides its blocks, in blocks (3 .. 6: within 3 %)
 constexpr int kMmaWarp = 8, kCopyWarp = 9;   // and 10: the second stream's products
+constexpr int kQueryWarp = 11;
 constexpr int kExpandWarp = 12;      // 12-15, for 8-bit rows only
 constexpr float kShift = 10.0f;      // weights are 2^10 times exp(s - max)
 constexpr float kLazy = 5.0f;        // a maximum may lag this far (log2)
@@ -198,19 +207,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// Barrier `id` among `n` threads; the OR of their flags.
+// Barrier `id` among `n` threads.
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ bool group_or(int id, int n, bool flag)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
-        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(n), "r"(flag ? 1 : 0)
-        : "memory");
-    return r != 0;
-}
 
 // Order of a segment's tiles in the ring: step i asks for the values of block
 // i - lag and the keys of block i (lag 1: both streams on every block; 2: a
@@ -231,7 +229,10 @@ struct Barriers {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t raw_full[8], raw_empty[8];   // 8-bit rows: the copies' ring of codes
     uint64_t scale_full[16];              // and the blocks' scales
-    uint64_t q_full;          // queries of a segment are in shared memory, the last outputs read
+    // Segments by their number's parity: a role that lags by one is never taken for one that does not.
+    uint64_t q_full[2];       // a segment's queries are in shared memory
+    uint64_t q_empty;         // both streams' products have read them
+    uint64_t seg_done[2];     // a segment's outputs are written
     uint64_t s_full[2][2];    // a half of a stream's scores is in tensor memory
     uint64_t p_full[2][2];    // a half of its weights is
     uint64_t o_full[2][2];    // that half's product with values is done
@@ -259,7 +260,8 @@ struct Shared {
     uint32_t tmem;
     int gave_up;              // volatile use: a wait ran out somewhere
     int strange;              // a value row of the segment's nodes is not finite
-    Where where[5];           // the softmax groups, the streams' products, the copies, the expanding warps
+    int bad[2];               // a page id of the segment is out of range, or its request's length
+    Where where[6];           // the softmax groups, the streams' products, the copies, the expanding warps, the queries
     float m[kTile], l[kTile];
     int ve;
     // 8-bit rows, of each block kept: by 32 places, whose scales are not finite,
@@ -324,8 +326,10 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             mbar_init(&b.raw_empty[i], 4);
         }
         for (int i = 0; KIND == kKvQ8 && i < R::kScales; ++i) mbar_init(&b.scale_full[i], 4);
-        mbar_init(&b.q_full, 8);
+        mbar_init(&b.q_empty, 2);
         for (int x = 0; x < 2; ++x) {
+            mbar_init(&b.q_full[x], 1);
+            mbar_init(&b.seg_done[x], 8);
             mbar_init(&b.drain[x], 1);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&b.s_full[x][h], 1);
@@ -536,7 +540,9 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
     } else if (warp == kMmaWarp || warp == kMmaWarp + 2) {
         // ---------------- products: a warp to each stream runs the loop, one elected lane issues ----------------
         const int x = (warp - kMmaWarp) >> 1;
-        constexpr uint32_t kScoreDesc = mma_desc(64, false), kOutDesc = mma_desc(D, true);
+        constexpr uint32_t kOutDesc = mma_desc(D, true);
+        // A negative softmax scale turns the queries' signs (bit 13 negates A).
+        const uint32_t score_desc = mma_desc(64, false) | (p.scale_log2 < 0.0f ? 1u << 13 : 0u);
         const uint64_t qd = tile_desc(smem_u32(qbuf), 16), kd = tile_desc(smem_u32(ring), 16);
         const uint64_t vd = tile_desc(smem_u32(ring), R::kHalfBytes);
         const uint32_t s_at = tmem + 128 * x, o_at = tmem + 256 + D * x;
@@ -546,10 +552,14 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         uint32_t entry = 0, segs = 0, np = 0, commits = 0;   // np: phase of this stream's blocks
         bool ok = true;
         while (ok && at.next_for_warp(p)) {
-            if (seg.w.bad) continue;   // nothing to multiply, its outputs are NaN
-            if (!warp_wait_or_give_up(&b.q_full, segs++ & 1u, gave_up, p.status)) {
+            if (!warp_wait_or_give_up(&b.q_full[segs & 1u], (segs >> 1) & 1u, gave_up, p.status)) {
                 ok = false;
                 break;
+            }
+            ++segs;
+            if (seg.w.bad) {           // nothing to multiply, its outputs are NaN
+                if (lane == 0) mbar_arrive(&b.q_empty);
+                continue;
             }
             fence_after();
             const int nb = static_cast<int>(seg.nb);
@@ -567,29 +577,31 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 mma_commit(empty);
                 if (!two) mma_commit(empty);
             };
-            // s = q k^T of half h of a block (64 places).
-            auto scores = [&](uint64_t off, uint32_t sk, int h) {
+            // s = q k^T of half h of a block (64 places); the segment's last ones free the queries.
+            auto scores = [&](uint64_t off, uint32_t sk, int h, bool last) {
                 if (elect_one()) {
                     const uint64_t kx = kd + off + h * (64 * 128 >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t k16 = (ks >> 2) * (R::kHalfBytes >> 4) + (ks & 3) * 2;
-                        mma_ss(s_at + 64 * h, qx + k16, kx + k16, kScoreDesc, ks > 0);
+                        mma_ss(s_at + 64 * h, qx + k16, kx + k16, score_desc, ks > 0);
                     }
                     mma_commit(&b.s_full[x][h]);
                     if (h == 1) free_tile(sk);
+                    if (h == 1 && last) mma_commit(&b.q_empty);
                 }
                 __syncwarp();
                 ++commits;
             };
             const int i0 = two ? 0 : x;
+            if (i0 >= nb && lane == 0) mbar_arrive(&b.q_empty);
             if (i0 < nb) {
                 const uint32_t sk = seq_k(i0, lag);
                 const uint64_t off = wait_tile(sk);
                 if (!ok) break;
                 fence_after();
-                scores(off, sk, 0);
-                scores(off, sk, 1);
+                scores(off, sk, 0, false);
+                scores(off, sk, 1, i0 + step >= nb);
             }
             for (int i = i0; ok && i < nb; i += step, np ^= 1u) {
                 const uint32_t sv = seq_v(i, lag, nb), sk = seq_k(i + step, lag);
@@ -618,7 +630,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         if (h == 0) k_off = wait_tile(sk);
                         if (!ok) break;
                         fence_after();
-                        scores(k_off, sk, h);
+                        scores(k_off, sk, h, i + 2 * step >= nb);
                     }
                 }
             }
@@ -630,6 +642,64 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             if (lane == 0) mbar_wait_bounded(&b.drain[x], 0, nullptr);
             __syncwarp();
         }
+    } else if (warp == kQueryWarp) {
+        // ---------------- queries: to shared memory as the last segment's products are done with it ----------------
+        Where &at = sh.where[5];
+        const Segment &seg = at.seg;
+        if (lane == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
+        uint32_t segs = 0;
+        bool joined = false;                       // the last segment's end uses the queries' memory
+        while (at.next_for_warp(p)) {
+            if (segs > 0) {
+                const uint32_t last = segs - 1;
+                bool ok = warp_wait_or_give_up(&b.q_empty, last & 1u, gave_up, p.status);
+                if (segs > 1)                      // the one before it has long ended: at most two are in work
+                    ok = ok && warp_wait_or_give_up(&b.seg_done[(last - 1) & 1u], ((last - 1) >> 1) & 1u, gave_up, p.status);
+                if (joined) ok = ok && warp_wait_or_give_up(&b.seg_done[last & 1u], (last >> 1) & 1u, gave_up, p.status);
+                if (!ok) break;
+            }
+            const int valid = rows_of(seg);
+            bool bad = seg.w.bad;
+            joined = bad || valid <= kTile;
+            if (!bad) {
+                // Rows past the last one are zeros, and all are for a scale of 0.  A lane copies
+                // whole rows, 16 bytes at a time: the addresses are worked out once to a row.
+                const int64_t first_token = p.start[seg.r] < 0 ? 0 : p.start[seg.r];
+                const uint32_t group = static_cast<uint32_t>(p.group), base = static_cast<uint32_t>(seg.tile) * kRows;
+                const int rows = valid > kTile ? kRows : kTile;
+                const int there = p.scale_log2 == 0.0f ? 0 : valid;
+#pragma unroll 1
+                for (int r = lane; r < rows; r += 32) {
+                    const uint32_t rho = base + r, t = rho / group;
+                    const __half *src = r < there ? p.q + (first_token + t) * p.q_stride +
+                                                        (static_cast<int64_t>(seg.kvh) * group + (rho - t * group)) * D
+                                                  : p.q;
+                    const uint32_t dst = smem_u32(qbuf) + (r >> 7) * R::kTileBytes + (r & 127) * 128 + ((r & 7) << 4);
+                    const int bytes = r < there ? 16 : 0;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"((dst ^ ((c & 7) << 4)) + (c >> 3) * R::kHalfBytes),
+                                     "l"(src + 8 * c), "r"(bytes)
+                                     : "memory");
+                }
+                const int64_t used = (seg.w.len + (1 << p.page_shift) - 1) >> p.page_shift;
+                const int64_t lo = (seg.b0 * kBlock) >> p.page_shift;
+                const int64_t hi = (((seg.b0 + seg.nb) * kBlock - 1) >> p.page_shift) + 1;
+                for (int64_t i = lo + lane; i < hi && i < used; i += 32) {
+                    const int id = p.table[seg.r * p.width + i];
+                    bad |= id < 0 || id >= p.n_pages;
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            }
+            fence_async();
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                if (bad) atomicOr(p.status, kDevBadPage);
+                sh.bad[segs & 1u] = bad ? 1 : 0;
+                mbar_arrive(&b.q_full[segs & 1u]);
+            }
+            ++segs;
+        }
     }
     } else {
         // ---------------- softmax: a thread to a row ----------------
@@ -638,10 +708,9 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         const int wt = tid & 127;                  // lane of tensor memory: row within the stream's tile
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t s_at = tmem + lanes + 128 * x, o_at = tmem + lanes + 256 + D * x;
-        // A negative scale turns the queries' signs; scale 0 clears them.
+        // A negative scale turns the queries' signs in the products; scale 0 clears them.
         const float scale = p.scale_log2 == 0.0f ? 1.0f : fabsf(p.scale_log2);
-        const uint32_t q_and = p.scale_log2 == 0.0f ? 0u : 0xffffffffu, q_xor = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-        uint32_t entry = 0, ns = 0;                // ring entries so far; phase of this stream's blocks
+        uint32_t entry = 0, ns = 0, segs = 0;      // ring entries so far; phase of this stream's blocks; segments
         bool ok = true;
         Where &at = sh.where[0];
         const Segment &seg = at.seg;
@@ -658,47 +727,8 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             const int64_t len = seg.w.len, ctx = len - seg.w.nodes, b0 = seg.b0;
             const int64_t first_token = p.start[seg.r] < 0 ? 0 : p.start[seg.r];
             const int64_t row_base = static_cast<int64_t>(seg.tile) * kRows;
-            // ---- queries to shared memory; rows past the last one are zeros ----
-            bool bad = seg.w.bad;
-            if (!bad) {
-                // a thread's 16-byte chunk is the same in each of its rows; eight loads in flight
-                constexpr int kStride = 256 / (D / 8);
-                const int c = tid & (D / 8 - 1);
-                for (int r0 = tid / (D / 8); r0 < (two ? kRows : kTile); r0 += 8 * kStride) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = r0 + k * kStride;
-                        v[k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < valid) {
-                            const uint32_t rho = static_cast<uint32_t>(row_base) + r, t = rho / static_cast<uint32_t>(p.group);
-                            v[k] = *reinterpret_cast<const uint4 *>(
-                                p.q + (first_token + t) * p.q_stride + (seg.kvh * p.group + (rho - t * p.group)) * D + 8 * c);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = (r0 + k * kStride) & 127;
-                        const uint4 u = make_uint4((v[k].x & q_and) ^ q_xor, (v[k].y & q_and) ^ q_xor,
-                                                   (v[k].z & q_and) ^ q_xor, (v[k].w & q_and) ^ q_xor);
-                        *reinterpret_cast<uint4 *>(qbuf + ((r0 + k * kStride) >> 7) * R::kTileBytes + (c >> 3) * R::kHalfBytes +
-                                                   r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
-                    }
-                }
-                const int64_t used = (len + (1 << p.page_shift) - 1) >> p.page_shift;
-                const int64_t lo = (seg.b0 * kBlock) >> p.page_shift;
-                const int64_t hi = (((seg.b0 + nb) * kBlock - 1) >> p.page_shift) + 1;
-                for (int64_t i = lo + tid; i < hi && i < used; i += 256) {
-                    const int id = p.table[seg.r * p.width + i];
-                    bad |= id < 0 || id >= p.n_pages;
-                }
-            }
-            fence_async();
-            fence_before();
-            bad = group_or(1, 256, bad);
-            if (bad && tid == 0) atomicOr(p.status, kDevBadPage);
-            __syncwarp();
-            if (lane == 0 && !seg.w.bad) mbar_arrive(&b.q_full);
+            ok = warp_wait_or_give_up(&b.q_full[segs & 1u], (segs >> 1) & 1u, gave_up, p.status) && ok;
+            const bool bad = seg.w.bad || !ok || sh.bad[segs & 1u] != 0;
 
             const int row = (two ? kTile * x : 0) + wt;              // row of the unit
             const int64_t rho = row_base + row;
@@ -992,7 +1022,10 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             }
             if (tid == 0) sh.strange = 0;
             fence_before();
-            group_sync(1, 256);                    // the queries' memory may be written again
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.seg_done[segs & 1u]);
+            ++segs;
+            group_sync(1, 256);                    // nobody reads this segment's record any more
         }
         if (tid == 0 && !left_unit) workspace_units(p)[blockIdx.x].parts = 0;
     }
