@@ -24,7 +24,7 @@
 // scales multiply scores and weights in fp32, weights are held below fp16's
 // largest value by a running power of two, which enters through the exponent.
 // The scales' arithmetic makes the softmax longer still: the chunks and the eight
-// trees of the figures below take 248 and 145 us, the 16 nodes 201.
+// trees of the figures below take 244 and 138 us, the 16 nodes 201.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
 // the copies, 11 brings the next segment's queries as soon as the last products
 // have read this one's (loaded by the softmax groups at a segment's start instead,
@@ -132,6 +132,16 @@ __device__ __forceinline__ void st_32cols(uint32_t taddr, const uint32_t *v)
           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
           "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]),
           "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void st_16cols(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 
@@ -848,6 +858,9 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                                     sum[0] = add2(sum[0], sum[1]);
                                     l_half += (low(sum[0]) + high(sum[0])) * exp2_fast(-by);
                                     t[g] = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) - (c0 + by);
+                                    // stored at once: fewer registers (eight trees 146 -> 138 us; fp16
+                                    // rows, which have them, gain nothing)
+                                    st_16cols(s_at + 64 * h + 16 * g, w + 16 * g);
                                 }
                                 top = fmaxf(t[0], t[1]);
                             }
@@ -875,7 +888,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                             vfix = 1.0f;
                         }
                         if (!ok) break;
-                        st_32cols(s_at + 64 * h, w);
+                        if constexpr (KIND == kKvF16) st_32cols(s_at + 64 * h, w);
                         l += l_half;
                     }
                     if (KIND == kKvF16 && masked && (wt >> 6) == h && j0 + wt >= ctx) {
