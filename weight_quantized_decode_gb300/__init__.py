@@ -631,14 +631,14 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
         raise ValueError(f"{fn}: qkv must be [T, (n_heads + 2 * {hk}) * {D}] with dense rows")
     T, wide = shape
     slots_ptr = _int32(fn, "slots", slots, 1, at)
-    if len(slots) != T:
+    if slots.shape[0] != T:
         raise ValueError(f"{fn}: one slot to a token")
     pos_ptr = cos_ptr = sin_ptr = n_pos = rot = 0
     if (cos is None) != (sin is None) or (cos is not None and pos is None):
         raise ValueError(f"{fn}: a rotation takes pos, cos and sin")
     if cos is not None:
         pos_ptr = _int32(fn, "pos", pos, 1, at)
-        if len(pos) != T:
+        if pos.shape[0] != T:
             raise ValueError(f"{fn}: one position to a token")
         if not (cos.get_device() == sin.get_device() == at and cos.dtype is torch.float32 and sin.dtype is torch.float32
                 and cos.dim() == 2 and cos.shape == sin.shape and cos.is_contiguous() and sin.is_contiguous()):
@@ -691,11 +691,11 @@ def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=Non
     table_ptr, start_ptr = _int32(fn, "table", table, 2, at), _int32(fn, "start", start, 1, at)
     R, width = table.shape
     len_ptr = _int32(fn, "kv_len", kv_len, 1, at)
-    if len(start) != R + 1 or len(kv_len) != R:
+    if start.shape[0] != R + 1 or kv_len.shape[0] != R:
         raise ValueError(f"{fn}: table [R, width], start [R + 1] and kv_len [R] must agree")
     tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, T, at)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif not (out.get_device() == at and out.dtype is torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
         raise ValueError(f"{fn}: out must be a contiguous CUDA float16 tensor of {T}x{H}x{D}")
     if workspace is None:
