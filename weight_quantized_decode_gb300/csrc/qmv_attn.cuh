@@ -286,14 +286,15 @@ __host__ __device__ __forceinline__ uint32_t seen_places(const int32_t *tree_row
 }
 
 // Bounded wait that also gives up when another role of the CTA has.
-__device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status)
+__device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status,
+                                                unsigned long long limit_ns = kWaitLimitNs)
 {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait_sleep(bar, parity, kSuspendHintNs)) return true;
         if (*gave_up) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (global_timer_ns() - t0 > limit_ns) {
             *gave_up = 1;
             atomicOr(status, kDevTimeout);
             return false;
@@ -302,11 +303,12 @@ __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity, 
 }
 
 // The same for a whole warp: every lane calls it and gets the same answer.
-__device__ __forceinline__ bool warp_wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status)
+__device__ __forceinline__ bool warp_wait_or_give_up(uint64_t *bar, uint32_t parity, volatile int *gave_up, int *status,
+                                                     unsigned long long limit_ns = kWaitLimitNs)
 {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = wait_or_give_up(bar, parity, gave_up, status);
+    if ((threadIdx.x & 31) == 0) ok = wait_or_give_up(bar, parity, gave_up, status, limit_ns);
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     if (ok)   // the phase has completed: every lane observes it before going on
         while (!mbar_try_wait(bar, parity)) {

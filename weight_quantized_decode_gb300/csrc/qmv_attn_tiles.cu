@@ -659,10 +659,14 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         if (lane == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         uint32_t segs = 0;
         bool joined = false;                       // the last segment's end uses the queries' memory
+        int64_t blocks = 0;                        // of the last segment
         while (at.next_for_warp(p)) {
             if (segs > 0) {
                 const uint32_t last = segs - 1;
-                bool ok = warp_wait_or_give_up(&b.q_empty, last & 1u, gave_up, p.status);
+                // This wait lasts as long as the last segment does, some 2 us a block (each
+                // other role's waits are for one step of the pipeline): its limit grows with it.
+                const unsigned long long limit = kWaitLimitNs + static_cast<unsigned long long>(blocks) * 100000ull;
+                bool ok = warp_wait_or_give_up(&b.q_empty, last & 1u, gave_up, p.status, limit);
                 if (segs > 1)                      // the one before it has long ended: at most two are in work
                     ok = ok && warp_wait_or_give_up(&b.seg_done[(last - 1) & 1u], ((last - 1) >> 1) & 1u, gave_up, p.status);
                 if (joined) ok = ok && warp_wait_or_give_up(&b.seg_done[last & 1u], (last >> 1) & 1u, gave_up, p.status);
@@ -671,6 +675,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             const int valid = rows_of(seg);
             bool bad = seg.w.bad;
             joined = bad || valid <= kTile;
+            blocks = seg.nb;
             if (!bad) {
                 // Rows past the last one are zeros, and all are for a scale of 0.  A lane copies
                 // whole rows, 16 bytes at a time: the addresses are worked out once to a row.
