@@ -24,7 +24,7 @@
 // scales multiply scores and weights in fp32, weights are held below fp16's
 // largest value by a running power of two, which enters through the exponent.
 // The scales' arithmetic makes the softmax longer still: the chunks and the eight
-// trees of the figures below take 244 and 138 us, the 16 nodes 201.
+// trees of the figures below take 240 and 138 us, the 16 nodes 190 to 200.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
 // the copies, 11 brings the next segment's queries as soon as the last products
 // have read this one's (loaded by the softmax groups at a segment's start instead,
@@ -80,11 +80,12 @@ struct Ring {
     static constexpr int kScaleAt = kRawAt + kRaw * kRawBytes;
     static constexpr size_t kSmem = 1024 + (KIND == kKvF16 ? kRawAt : kScaleAt + kScales * 2 * kBlock * 4);
     // Registers of a thread: at launch, and after the softmax groups have taken
-    // what the others give up (the shares add up to the launch's).
+    // what the others give up (the shares add up to the launch's; these leave least in
+    // local memory, and 224 and 56, or 176, 64 and 96, measured up to 1 % slower).
     static constexpr int kThreads = KIND == kKvF16 ? 384 : 512;
     static constexpr int kLaunchRegs = KIND == kKvF16 ? 168 : 128;
-    static constexpr int kSoftmaxRegs = KIND == kKvF16 ? 224 : 176, kOtherRegs = KIND == kKvF16 ? 56 : 64;
-    static constexpr int kExpandRegs = 96;
+    static constexpr int kSoftmaxRegs = KIND == kKvF16 ? 208 : 176, kOtherRegs = KIND == kKvF16 ? 88 : 80;
+    static constexpr int kExpandRegs = 80;
     static_assert(2 * kSoftmaxRegs + kOtherRegs + (KIND == kKvF16 ? 0 : kExpandRegs) == kThreads / 128 * kLaunchRegs,
                   "shares of the launch's registers");
 };
