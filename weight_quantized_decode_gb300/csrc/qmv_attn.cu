@@ -59,9 +59,9 @@ cudaError_t launch_tree_attn(const AttnParams &p, int D, int kind, int sms, cuda
     // Rows that share a key/value head in the average request: up to 32 are one
     // unit of the streaming kernel; more go to the 128-row tiles.  Measured, 32
     // heads on 8 of 128, streaming against tiles: one request of 30001 places,
-    // 32 rows 36 against 39 us, 64 rows 43 against 43, 128 rows 69 against 51;
-    // 16 requests of 4000, 32 rows 57 against 65, 48 rows 83 against 69; 8-bit
-    // rows the same way (32 rows 57 against 80, 48 rows 96 against 83).
+    // 32 rows 36 against 39 us, 48 rows 44 against 42, 128 rows 71 against 50;
+    // 16 requests of 4000, 32 rows 57 against 61, 48 rows 85 against 65; 8-bit
+    // rows the same way (32 rows 57 against 89, 48 rows 98 against 89).
     const int64_t rows = (p.T + p.R - 1) / p.R * p.group;
     if (rows <= 32) return launch_attn_rows(p, D, kind, rows, sms, s, pdl);
     return launch_attn_tiles(p, D, kind, sms, s, pdl);
