@@ -581,6 +581,20 @@ def _call_on(fn, index, stream, args):
         raise QmvError(fn, code)
 
 
+def _side_stream(index, stream):
+    """The stream of a call as torch has it, where it is not device `index`'s current one; else None.  Memory for the
+    call alone is then allocated under it: the allocator gives a freed block to the next tensor of the stream it was
+    allocated under, in that stream's order, and any other stream's work could still be using it."""
+    if stream is None:
+        return None
+    torch, handle = _torch(), _stream_handle(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
+
+
 def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n_pages=None, stream=None):
     """Page and slot maps of one step, on the GPU.  lens, n_new [R]; free [n], ids of unused pages, taken in order
     from index `head` ([1], default 0) on; table [R, width] is completed in place; tokens: length of the per-token
@@ -699,7 +713,8 @@ def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=Non
     elif not (out.get_device() == at and out.dtype is torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
         raise ValueError(f"{fn}: out must be a contiguous CUDA float16 tensor of {T}x{H}x{D}")
     if workspace is None:
-        workspace = qmv_tree_attn_workspace(cache.device)
+        with torch.cuda.stream(_side_stream(at, stream)):     # (None: the current stream)
+            workspace = qmv_tree_attn_workspace(cache.device)
     elif workspace.get_device() != at or not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be a contiguous CUDA tensor")
     k, v, ks, vs = cache._ptrs()
