@@ -595,6 +595,20 @@ def _side_stream(index, stream):
     return torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
 
 
+def _output(shape, dtype, device, index, stream):
+    """An output of a call on `stream`: memory that nothing before the call on that stream can still be using, and that
+    is not given away, once freed, before the current stream's work up to then is done."""
+    torch = _torch()
+    side = _side_stream(index, stream)
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    reader = torch.cuda.current_stream(index)
+    with torch.cuda.stream(side):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(reader)
+    return out
+
+
 def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n_pages=None, stream=None):
     """Page and slot maps of one step, on the GPU.  lens, n_new [R]; free [n], ids of unused pages, taken in order
     from index `head` ([1], default 0) on; table [R, width] is completed in place; tokens: length of the per-token
@@ -616,7 +630,9 @@ def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n
         if head.shape[0] != 1:
             raise ValueError(f"{fn}: head must be one number")
     tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, tokens, at)
-    out = torch.empty(2 * R + 2 + 3 * tokens, dtype=torch.int32, device=lens.device)
+    size = 2 * R + 2 + 3 * tokens
+    out = torch.empty(size, dtype=torch.int32, device=lens.device) if stream is None else \
+        _output(size, torch.int32, lens.device, at, stream)
     o, n = out.data_ptr(), 4 * tokens
     s = o + 4 * (2 * R + 1)
     _call_on(fn, at, stream,
@@ -661,7 +677,8 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
         rot *= 2
         cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
     if q is None:
-        q = torch.empty((T, n_heads, D), dtype=torch.float16, device=cache.device)
+        q = torch.empty((T, n_heads, D), dtype=torch.float16, device=cache.device) if stream is None else \
+            _output((T, n_heads, D), torch.float16, cache.device, at, stream)
     elif not (q.get_device() == at and q.dtype is torch.float16 and q.is_contiguous() and q.numel() == T * n_heads * D):
         raise ValueError(f"{fn}: q must be a contiguous CUDA float16 tensor of {T}x{n_heads}x{D}")
     k, v, ks, vs = cache._ptrs()
@@ -709,7 +726,8 @@ def qmv_tree_attn(q, cache, table, start, kv_len, tree=None, scale=None, out=Non
         raise ValueError(f"{fn}: table [R, width], start [R + 1] and kv_len [R] must agree")
     tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, T, at)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if stream is None else \
+            _output(shape, torch.float16, cache.device, at, stream)
     elif not (out.get_device() == at and out.dtype is torch.float16 and out.is_contiguous() and out.numel() == T * H * D):
         raise ValueError(f"{fn}: out must be a contiguous CUDA float16 tensor of {T}x{H}x{D}")
     if workspace is None:
