@@ -709,6 +709,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             }
             fence_async();
             bad = __any_sync(0xffffffffu, bad);
+            __syncwarp();                          // all lanes' copies before lane 0 says so (a vote orders no memory)
             if (lane == 0) {
                 if (bad) atomicOr(p.status, kDevBadPage);
                 sh.bad[segs & 1u] = bad ? 1 : 0;
