@@ -41,3 +41,52 @@ def seeing(prob, node, nodes):
 # (query heads on one key/value head, columns, tokens): 8, 16 and 32 rows, one tile of
 # 128 rows and two, and one request whose rows are several units
 ROWS = [(2, 64, 3), (4, 128, 4), (2, 128, 16), (3, 64, 40), (4, 128, 60), (4, 64, 150)]
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("tree", [None, "random"])
+@pytest.mark.parametrize("heads,D,T", ROWS + [(1, 128, 300)])
+@pytest.mark.parametrize("ctx", [0, 50, 3000])
+def test_one_value_that_is_not_finite(q, ws, ctx, heads, D, T, tree, bad):
+    """fp16 rows: nodes with one infinity or NaN each, in columns of their own.
+    The other columns count once, for every token, and the bad ones only for
+    tokens that see them; the same on every run."""
+    prob = ref.problem([ctx], [T], heads, 1, D, 16, tree=tree, seed=T, words=10 if tree else None)
+    nodes = sorted({1, T // 3, T // 2, T - 1})
+    clean, p = copy(prob), copy(prob)
+    for column, node in enumerate(nodes):
+        at = (prob["table"][0, (ctx + node) // 16], 0, (ctx + node) % 16, 7 * column)
+        clean["v"][at], p["v"][at] = 0.0, bad
+    want, allow = ref.attention(clean, D ** -0.5)
+    first = call(q, p, ws)
+    got = first.cpu().numpy().astype(np.float64)
+    shown = np.zeros(got.shape, dtype=bool)
+    for column, node in enumerate(nodes):
+        shown[seeing(p, node, T), :, 7 * column] = True
+    assert not np.isfinite(got[shown]).any()
+    assert np.all(np.abs(got - want)[~shown] <= allow[~shown])
+    for _ in range(10):
+        again = call(q, p, ws)
+        assert torch.equal(first.view(torch.int16)[torch.from_numpy(~shown).cuda()],
+                           again.view(torch.int16)[torch.from_numpy(~shown).cuda()])
+    assert q.qmv_device_status() == 0
+
+
+def test_requests_with_such_a_value_between_others(q, ws):
+    """Units with and without one in turn on the same blocks of threads."""
+    R, T = 200, 80
+    prob = ref.problem([(5 * r) % 60 for r in range(R)], [T] * R, 8, 4, 64, 16, seed=5)
+    clean, p = copy(prob), copy(prob)
+    for r in range(0, R, 3):
+        j = int(prob["kv_len"][r]) - T + 1
+        at = (prob["table"][r, j // 16], slice(None), j % 16, 9)
+        clean["v"][at], p["v"][at] = 0.0, np.inf
+    want, allow = ref.attention(clean, 0.125)
+    for _ in range(5):
+        got = call(q, p, ws).cpu().numpy().astype(np.float64)
+        shown = np.zeros(got.shape, dtype=bool)
+        for r in range(0, R, 3):
+            shown[r * T + 1:(r + 1) * T, :, 9] = True
+        assert not np.isfinite(got[shown]).any()
+        assert np.all(np.abs(got - want)[~shown] <= allow[~shown])
+    assert q.qmv_device_status() == 0

@@ -240,6 +240,7 @@ struct Barriers {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t raw_full[8], raw_empty[8];   // 8-bit rows: the copies' ring of codes
     uint64_t scale_full[16];              // and the blocks' scales
+    uint64_t clean[8];                    // fp16 rows: the value tile in a slot has been looked over (the second stream waits)
     // Segments by their number's parity: a role that lags by one is never taken for one that does not.
     uint64_t q_full[2];       // a segment's queries are in shared memory
     uint64_t q_empty;         // both streams' products have read them
@@ -283,14 +284,28 @@ struct Shared {
     int exponent[16][4];
 };
 
+// Places below this one are seen by every row from `row` of the unit on.
+__device__ __forceinline__ int64_t open_places(const AttnParams &p, const Segment &s, int row)
+{
+    const int64_t ctx = s.w.len - s.w.nodes;
+    return p.tree ? ctx : ctx + (static_cast<uint32_t>(s.tile) * kRows + row) / static_cast<uint32_t>(p.group) + 1;
+}
+
+// The first block of a unit, of fp16 rows, whose value tile is looked over before
+// either stream multiplies it: the first that holds a place some row of the unit
+// does not see.  There rows past the end, and nodes' rows that are not finite, are
+// cleared, and the latter are what add_strange_nodes adds; both streams read the
+// tile, so which tiles these are does not depend on the stream.
+__device__ __forceinline__ int64_t first_cleaned(const AttnParams &p, const Segment &s) { return open_places(p, s, 0) / kBlock; }
+
 // Adds by hand what nodes with a non-finite value row (cleared for the products)
 // give to columns d0 .. d0 + 31 of a row: exact, and rare.
 template <int D>
 __device__ __forceinline__ void add_strange_nodes(const AttnParams &p, const Segment &seg, const __half *q,
                                                const int32_t *tree_row, int node, float c, int d0, float (&o)[32])
 {
-    const int64_t ctx = seg.w.len - seg.w.nodes;
-    const int64_t lo = seg.b0 * kBlock, hi = (seg.b0 + seg.nb) * kBlock;
+    const int64_t ctx = seg.w.len - seg.w.nodes, cleaned = first_cleaned(p, seg);
+    const int64_t lo = (seg.b0 > cleaned ? seg.b0 : cleaned) * kBlock, hi = (seg.b0 + seg.nb) * kBlock;
     const int page = 1 << p.page_shift;
     for (int64_t j = lo > ctx ? lo : ctx; j < hi && j < seg.w.len; ++j) {
         if (!(seen_places(tree_row, p.tree_words, node, seg.w.nodes, seg.w.len, j) & 1u)) continue;
@@ -331,6 +346,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         for (int i = 0; i < R::kSlots; ++i) {
             mbar_init(&b.kv_full[i], KIND == kKvF16 ? 1 : 4);
             mbar_init(&b.kv_empty[i], 2);
+            mbar_init(&b.clean[i], 4);
         }
         for (int i = 0; KIND == kKvQ8 && i < R::kRaw; ++i) {
             mbar_init(&b.raw_full[i], 1);
@@ -349,7 +365,6 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             }
         }
         sh.gave_up = 0;
-        sh.strange = 0;
         mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -561,6 +576,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         const Segment &seg = at.seg;
         if (lane == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         uint32_t entry = 0, segs = 0, np = 0, commits = 0;   // np: phase of this stream's blocks
+        uint32_t cleans = 0;                       // phases of the slots' barriers `clean`, a bit to a slot
         bool ok = true;
         while (ok && at.next_for_warp(p)) {
             if (!warp_wait_or_give_up(&b.q_full[segs & 1u], (segs >> 1) & 1u, gave_up, p.status)) {
@@ -604,6 +620,8 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 __syncwarp();
                 ++commits;
             };
+            // Blocks from here on: the first stream's softmax group looks the value tile over for both.
+            const int64_t looked = KIND == kKvF16 && two && x == 1 ? first_cleaned(p, seg) - seg.b0 : nb;
             const int i0 = two ? 0 : x;
             if (i0 >= nb && lane == 0) mbar_arrive(&b.q_empty);
             if (i0 < nb) {
@@ -618,6 +636,11 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 const uint32_t sv = seq_v(i, lag, nb), sk = seq_k(i + step, lag);
                 const bool more = i + step < nb;
                 const uint64_t v_off = wait_tile(sv);
+                if (i >= looked) {
+                    const uint32_t slot = (entry + sv) % R::kSlots;
+                    ok = ok && warp_wait_or_give_up(&b.clean[slot], cleans >> slot & 1u, gave_up, p.status);
+                    cleans ^= 1u << slot;
+                }
                 uint64_t k_off = 0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -734,7 +757,10 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
         bool left_unit = false;                    // word of a shared unit left for the second kernel
         if (tid == 0) at.walk.begin(p, sh.share, static_cast<int>(blockIdx.x));
         while (true) {
-            if (tid == 0) at.more = at.walk.next(p, at.seg) ? 1 : 0;
+            if (tid == 0) {
+                at.more = at.walk.next(p, at.seg) ? 1 : 0;
+                sh.strange = 0;                    // (all have read the last segment's)
+            }
             group_sync(1, 256);
             if (!at.more) break;
             const int valid = rows_of(seg);
@@ -755,8 +781,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             // what they give goes to rows that nobody reads.
             const bool idle = row - lane >= valid;
             // Places below `open` are seen by every row of this stream.
-            const int64_t open =
-                p.tree ? ctx : ctx + static_cast<uint32_t>(row_base + (two ? kTile * x : 0)) / static_cast<uint32_t>(p.group) + 1;
+            const int64_t open = open_places(p, seg, two ? kTile * x : 0);
             float m = -INFINITY, l = 0.0f;
             bool first = true;
             int ve = -126;                         // 8-bit rows: 2^ve is at least the largest value scale so far
@@ -898,34 +923,41 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         if constexpr (KIND == kKvF16) st_32cols(s_at + 64 * h, w);
                         l += l_half;
                     }
-                    if (KIND == kKvF16 && masked && (wt >> 6) == h && j0 + wt >= ctx) {
+                    if (KIND == kKvF16 && masked && h == 0 && (x == 0 || !two)) {
                         // Value rows past the end are cleared, and so are nodes' rows
-                        // that are not finite (add_strange_nodes adds those).
-                        const uint32_t e = entry + seq_v(i, lag, nb);
-                        ok = ok && wait_or_give_up(&b.kv_full[e % R::kSlots], (e / R::kSlots) & 1u, gave_up, p.status);
-                        uint8_t *v = ring + (e % R::kSlots) * R::kTileBytes + wt * 128;
-                        bool clear = j0 + wt >= len;
-                        if (ok && !clear) {
+                        // that are not finite (add_strange_nodes adds those): before this
+                        // stream's product, and where the other reads the tile as well,
+                        // before it is told that the tile is clean.
+                        const uint32_t e = entry + seq_v(i, lag, nb), slot = e % R::kSlots;
+                        if (j0 + wt >= ctx) {
+                            ok = ok && wait_or_give_up(&b.kv_full[slot], (e / R::kSlots) & 1u, gave_up, p.status);
+                            uint8_t *v = ring + slot * R::kTileBytes + wt * 128;
+                            bool clear = j0 + wt >= len;
+                            if (ok && !clear) {
 #pragma unroll
-                            for (int hh = 0; hh < R::kHalves; ++hh)
+                                for (int hh = 0; hh < R::kHalves; ++hh)
 #pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const uint4 q4 =
-                                        *reinterpret_cast<const uint4 *>(v + hh * R::kHalfBytes + ((c ^ (wt & 7)) << 4));
-                                    const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
+                                    for (int c = 0; c < 8; ++c) {
+                                        const uint4 q4 =
+                                            *reinterpret_cast<const uint4 *>(v + hh * R::kHalfBytes + ((c ^ (wt & 7)) << 4));
+                                        const uint32_t u[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        clear |= (u[k] & 0x7c00u) == 0x7c00u || (u[k] & 0x7c000000u) == 0x7c000000u;
-                                }
-                            if (clear) sh.strange = 1;
+                                        for (int k = 0; k < 4; ++k)
+                                            clear |= (u[k] & 0x7c00u) == 0x7c00u || (u[k] & 0x7c000000u) == 0x7c000000u;
+                                    }
+                                if (clear) sh.strange = 1;
+                            }
+                            if (ok && clear)
+#pragma unroll
+                                for (int hh = 0; hh < R::kHalves; ++hh)
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c)
+                                        *reinterpret_cast<uint4 *>(v + hh * R::kHalfBytes + (c << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                            fence_async();
                         }
-                        if (ok && clear)
-#pragma unroll
-                            for (int hh = 0; hh < R::kHalves; ++hh)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    *reinterpret_cast<uint4 *>(v + hh * R::kHalfBytes + (c << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_async();
+                        ok = __all_sync(0xffffffffu, ok);
+                        __syncwarp();
+                        if (two && ok && lane == 0) mbar_arrive(&b.clean[slot]);
                     }
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -1040,7 +1072,6 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 left_unit = true;
                 leave_unit(p, seg, valid, first_token);
             }
-            if (tid == 0) sh.strange = 0;
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.seg_done[segs & 1u]);
