@@ -458,8 +458,10 @@ QMV_API int64_t qmv_tree_attn_workspace(void);
  *           multiple of 8.  out: fp16 [T][Hq][D].
  *   scale : HOST pointer to the softmax scale, read before the call returns
  *           (NULL: 1 / sqrt(D)).
- * Scores, maxima, sums and outputs are held in fp32; the weights p enter the
- * value product rounded to fp16, and the output is rounded once.
+ * Scores, maxima, sums and outputs are held in fp32; the weights p (8-bit rows:
+ * times their value scale) enter the value product rounded to fp16, of which
+ * half a subnormal step is 2^-35 of the largest weight's (8-bit rows: times the
+ * largest value scale that the token sees); the output is rounded once.
  * Rows of `out` past start[R] are left as they are.  A request whose page ids
  * leave [0, n_pages), or whose kv_len is below its new tokens or above
  * width * page, gets NaN (QMV_DEV_BAD_PAGE); other requests are unaffected.

@@ -90,3 +90,23 @@ def test_requests_with_such_a_value_between_others(q, ws):
         assert not np.isfinite(got[shown]).any()
         assert np.all(np.abs(got - want)[~shown] <= allow[~shown])
     assert q.qmv_device_status() == 0
+
+
+@pytest.mark.parametrize("big", [1e6, 1e10, 1e30, 2e36])
+@pytest.mark.parametrize("tree", [None, "random"])
+@pytest.mark.parametrize("heads,D,T", ROWS)
+@pytest.mark.parametrize("ctx", [0, 50, 3000])
+def test_large_value_scales_of_unseen_nodes(q, ws, ctx, heads, D, T, tree, big):
+    """8-bit rows: a node whose value row has a large finite scale leaves the
+    tokens that do not see it within the allowance of what they do see."""
+    prob = ref.problem([ctx], [T], heads, 1, D, 16, q8=True, tree=tree, seed=T, words=5 if tree else None)
+    for node in {T - 1, T // 2, 1}:
+        p = copy(prob)
+        at = ctx + node
+        p["v_scale"][p["table"][0, at // 16], :, at % 16] = big
+        off = ~seeing(p, node, T)
+        assert off.any()
+        want, allow = ref.attention(prob, D ** -0.5)
+        got = call(q, p, ws).cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got[off] - want[off]) <= allow[off]), (node, np.nanmax(np.abs(got[off] - want[off])))
+    assert q.qmv_device_status() == 0

@@ -17,8 +17,11 @@
 // the sum.  The maximum may lag by 2^5 before the outputs are rescaled.
 //   8-bit rows: codes become exact fp16 integers in registers.  The key scale
 // multiplies the score, the value scale the weight, both in fp32; weights are
-// held below fp16's largest value by a running power of two of the largest
-// value scale, handled like the running maximum.
+// held below fp16's largest value by a running power of two of the largest value
+// scale, handled like the running maximum.  It is one for all rows as long as they
+// see the same places; from the first step on where some see a larger scale than
+// before and others may not, each row has its own, in shared memory (the last steps
+// of a request; in registers for every step: 60 for 56 us, 16 requests with 32 rows).
 //   Measured: 64 requests of 100 to 16383 8-bit places, one token of 32 heads on
 // 8 of 128: 185 us, 6.1 TB/s, 0.90 of the measured copy bandwidth; 16 uneven
 // trees of up to 24 nodes over 511 to 8191 fp16 places, 16 heads on 8: 63 us,
@@ -98,6 +101,21 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t flipped, uint32_t se
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Bits of the magnitude of a finite value scale, else 0; the exponent e of 2^e
+// above a scale of these bits (-126 .. 126); 2^-e and back.
+__device__ __forceinline__ uint32_t finite_bits(float v)
+{
+    const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
+    return bits < 0x7f800000u ? bits : 0u;
+}
+__device__ __forceinline__ int exponent_above(uint32_t bits)
+{
+    const int e = static_cast<int>(bits >> 23) - 126;
+    return e > 126 ? 126 : e;
+}
+__device__ __forceinline__ float unit_of(int e) { return __uint_as_float(static_cast<uint32_t>(127 - e) << 23); }
+__device__ __forceinline__ int exponent_of_unit(float u) { return 127 - static_cast<int>(__float_as_uint(u) >> 23); }
+
 // Over the eight lanes that hold a column of a product's tile.
 __device__ __forceinline__ float column_max(float v)
 {
@@ -135,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
     __shared__ Share sh;
     __shared__ uint64_t bars[kWarps][R::kSlots];
     __shared__ float ml[2][kWarps][kRows];
+    __shared__ float units[kWarps][kRows];   // 8-bit rows: each row's 2^-ve, once they have their own
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -342,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             l[n][0] = l[n][1] = 0.0f;
         }
         int ve = -126;        // 8-bit: 2^ve is at least the largest value scale so far
+        bool own_units = false;
 
         // The entry that is due, as the address of its slot.
         auto wait_entry = [&]() {
@@ -462,21 +482,47 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
                     rises |= top[n][i] > m[n][i] + kLazy;
                 }
             const uint32_t vb = wait_entry();
-            float vfix = 1.0f, vunit = 1.0f;
+            float vfix = 1.0f;
             if constexpr (KIND == kKvQ8) {
                 float mine = lds1(scales_at + 4 * (slot * kStep + lane));
                 if (masked && j0 + lane >= len) mine = 0.0f;
-                const uint32_t bits = __float_as_uint(mine) & 0x7fffffffu;
                 // largest finite scale of the step; a non-finite one makes its own weights non-finite
-                const uint32_t most = __reduce_max_sync(0xffffffffu, bits < 0x7f800000u ? bits : 0u);
-                int e = static_cast<int>(most >> 23) - 126;
-                e = e > 120 ? 120 : e;
-                if (e > ve) {
+                const int e = exponent_above(__reduce_max_sync(0xffffffffu, finite_bits(mine)));
+                if (e > ve && !masked) {
                     vfix = exp2_fast(static_cast<float>(ve - e));
                     ve = e;
                     rises = true;
+                } else if (e > ve) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float &unit = units[warp][8 * n + 2 * t4 + i];
+                            const int before = own_units ? exponent_of_unit(unit) : ve;
+                            uint32_t most = 0u;   // of the places that this row sees
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t bits = finite_bits(lds1(scales_at + 4 * (slot * kStep + 8 * k + g)));
+                                if ((see[n][i] >> (8 * k) & 1u) && bits > most) most = bits;
+                            }
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) {
+                                const uint32_t other = __shfl_xor_sync(0xffffffffu, most, d);
+                                most = other > most ? other : most;
+                            }
+                            const int seen = exponent_above(most), now = seen > before ? seen : before;
+                            const float f = exp2_fast(static_cast<float>(before - now));
+#pragma unroll
+                            for (int dt = 0; dt < KS; ++dt) {
+                                o[n][dt][i] *= f;
+                                o[n][dt][2 + i] *= f;
+                            }
+                            __syncwarp();         // every lane has read it
+                            if (g == 0) unit = unit_of(now);
+                        }
+                    own_units = true;
+                    __syncwarp();
                 }
-                vunit = __uint_as_float(static_cast<uint32_t>(127 - ve) << 23);   // 2^-ve
             }
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
@@ -513,14 +559,26 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             if constexpr (KIND == kKvQ8) {
 #pragma unroll
                 for (int pm = 0; pm < 2; ++pm) {
-                    const float d0 = lds1(scales_at + 4 * (slot * kStep + 16 * pm + g)) * vunit;
-                    const float d1 = lds1(scales_at + 4 * (slot * kStep + 16 * pm + 8 + g)) * vunit;
+                    const float d0 = lds1(scales_at + 4 * (slot * kStep + 16 * pm + g));
+                    const float d1 = lds1(scales_at + 4 * (slot * kStep + 16 * pm + 8 + g));
+                    if (!own_units) {
+                        const float e0 = d0 * unit_of(ve), e1 = d1 * unit_of(ve);
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        sc[n][pm][0] *= d0;
-                        sc[n][pm][1] *= d0;
-                        sc[n][pm][2] *= d1;
-                        sc[n][pm][3] *= d1;
+                        for (int n = 0; n < NR; ++n) {
+                            sc[n][pm][0] *= e0;
+                            sc[n][pm][1] *= e0;
+                            sc[n][pm][2] *= e1;
+                            sc[n][pm][3] *= e1;
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float unit = units[warp][8 * n + 2 * t4 + i];
+                                sc[n][pm][i] *= d0 * unit;
+                                sc[n][pm][2 + i] *= d1 * unit;
+                            }
                     }
                 }
                 if (masked) {
@@ -657,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
                 float most = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) most = fmaxf(most, ml[0][w][row]);
-                const float back = KIND == kKvQ8 ? __uint_as_float(static_cast<uint32_t>(ve + 127) << 23) : 1.0f;   // 2^ve
+                float back = 1.0f;            // 8-bit: the row's 2^ve
+                if constexpr (KIND == kKvQ8) back = unit_of(-(own_units ? exponent_of_unit(units[warp][row]) : ve));
                 const float f = m[n][i] == -INFINITY ? 0.0f : exp2_fast(m[n][i] - most) * back;
                 float *dst = oscr + (warp * kRows + row) * R::kOutPitch;
 #pragma unroll

@@ -22,7 +22,8 @@
 // then the weights simply come out larger, p <= 2^(10 + 5) < 65504.
 //   8-bit rows: a fourth warpgroup expands codes to fp16 tiles (exact integers);
 // scales multiply scores and weights in fp32, weights are held below fp16's
-// largest value by a running power of two, which enters through the exponent.
+// largest value by each row's running power of two of the largest value scale that
+// the row sees, which enters through the exponent.
 // The scales' arithmetic makes the softmax longer still: the chunks and the eight
 // trees of the figures below take 240 and 138 us, the 16 nodes 190 to 200.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
@@ -218,6 +219,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// 8-bit rows.  The value scales of 32 places are kept over a power of two, 2^e, e the
+// exponent above the largest of them or the nearer of these limits; weights carry
+// 2^(e - ve), ve the row's own.  So no step leaves fp32's range (2^(15 + 60 + 40) at
+// the most, where a node that the row does not see has a far larger scale), and what
+// lies below the lower limit is lost in the output's rounding to fp16.
+constexpr int kLeastExponent = -40, kMostKept = 60, kMostExponent = 126;
+
 // Barrier `id` among `n` threads.
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
@@ -275,13 +283,14 @@ struct Shared {
     int bad[2];               // a page id of the segment is out of range, or its request's length
     Where where[6];           // the softmax groups, the streams' products, the copies, the expanding warps, the queries
     float m[kTile], l[kTile];
-    int ve;
+    int ve[kTile];
     // 8-bit rows, of each block kept: by 32 places, whose scales are not finite,
-    // whose key scales are negative, and the exponent above the largest of the
-    // finite value scales
+    // whose key scales are negative, the exponent above the largest of the finite
+    // value scales, and the one that they are kept over
     uint32_t odd[16][4];
     uint32_t below[16][4];
     int exponent[16][4];
+    int kept[16][4];
 };
 
 // Places below this one are seen by every row from `row` of the unit on.
@@ -323,6 +332,31 @@ __device__ __forceinline__ void add_strange_nodes(const AttnParams &p, const Seg
 #pragma unroll
         for (int d = 0; d < 32; ++d) o[d] += w * __half2float(v[d0 + d]);
     }
+}
+
+// 8-bit rows: the exponent above the largest value scale that a row sees in a block of
+// 128 places (kept from vd on over the exponents from `over` on), not below `ve` and not
+// above `most_e`.
+__device__ __forceinline__ int seen_exponent(uint32_t vd, uint32_t over, int most_e, const int32_t *tree_row, int tree_words,
+                                          int node, int nodes, int64_t len, int64_t j0, int ve)
+{
+    int e = ve;
+#pragma unroll 1
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t see = seen_places(tree_row, tree_words, node, nodes, len, j0 + 32 * w);
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            const float4 d = lds4(vd + 128 * w + 4 * k);
+            if (see >> k & 1u) most = fmaxf(most, fabsf(d.x));
+            if (see >> k & 2u) most = fmaxf(most, fabsf(d.y));
+            if (see >> k & 4u) most = fmaxf(most, fabsf(d.z));
+            if (see >> k & 8u) most = fmaxf(most, fabsf(d.w));
+        }
+        const int own = static_cast<int>(__float_as_uint(most) >> 23) - 126 + static_cast<int>(__float_as_uint(lds1(over + 4 * w)));
+        if (own > e) e = own;
+    }
+    return e < most_e ? e : most_e;
 }
 
 template <int D, int KIND>
@@ -434,12 +468,13 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                         const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(vd) & 0x7fffffffu);
                         const uint32_t odd = __ballot_sync(0xffffffffu, there && !(k_finite && v_finite));
                         const uint32_t below = __ballot_sync(0xffffffffu, kd < 0.0f);
-                        int e = static_cast<int>(most >> 23) - 126;
-                        e = e > 120 ? 120 : e;
+                        const int e = static_cast<int>(most >> 23) - 126;
+                        const int over = e > kMostKept ? kMostKept : (e < kLeastExponent ? kLeastExponent : e);
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(kd) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * kBlock), "f"(vd * power_of_2(-e)) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + 4 * kBlock), "f"(vd * power_of_2(-over)) : "memory");
                         if (lane == 0) {
                             sh.exponent[kept][warp & 3] = e;
+                            sh.kept[kept][warp & 3] = over;
                             sh.odd[kept][warp & 3] = odd;
                             sh.below[kept][warp & 3] = below;
                         }
@@ -621,7 +656,8 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 ++commits;
             };
             // Blocks from here on: the first stream's softmax group looks the value tile over for both.
-            const int64_t looked = KIND == kKvF16 && two && x == 1 ? first_cleaned(p, seg) - seg.b0 : nb;
+            int64_t looked = 0;
+            if constexpr (KIND == kKvF16) looked = two && x == 1 ? first_cleaned(p, seg) - seg.b0 : nb;
             const int i0 = two ? 0 : x;
             if (i0 >= nb && lane == 0) mbar_arrive(&b.q_empty);
             if (i0 < nb) {
@@ -636,7 +672,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 const uint32_t sv = seq_v(i, lag, nb), sk = seq_k(i + step, lag);
                 const bool more = i + step < nb;
                 const uint64_t v_off = wait_tile(sv);
-                if (i >= looked) {
+                if (KIND == kKvF16 && i >= looked) {
                     const uint32_t slot = (entry + sv) % R::kSlots;
                     ok = ok && warp_wait_or_give_up(&b.clean[slot], cleans >> slot & 1u, gave_up, p.status);
                     cleans ^= 1u << slot;
@@ -784,26 +820,22 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             const int64_t open = open_places(p, seg, two ? kTile * x : 0);
             float m = -INFINITY, l = 0.0f;
             bool first = true;
-            int ve = -126;                         // 8-bit rows: 2^ve is at least the largest value scale so far
+            int ve = kLeastExponent;               // 8-bit rows: 2^ve is at least the largest value scale seen so far
             for (int i = two ? 0 : x; ok && i < nb; i += two ? 1 : 2, ns ^= 1u) {
                 const int64_t j0 = (b0 + i) * kBlock;
                 const bool masked = j0 + kBlock > open;
                 uint32_t kd = 0u, vd = 0u;                  // 8-bit rows: the block's scales, in shared memory
-                float vfix = 1.0f;
-                const int *ev = nullptr;                    // and the exponents of its value scales
+                const int *over = nullptr;                  // and the exponents that its value scales are kept over
+                int e_block = kLeastExponent;               // the largest exponent of its value scales
                 if constexpr (KIND == kKvQ8) {
                     const uint32_t block = entry / 2 + static_cast<uint32_t>(i), kept = block % R::kScales;
                     ok = warp_wait_or_give_up(&b.scale_full[kept], (block / R::kScales) & 1u, gave_up, p.status);
                     kd = smem_u32(smem + R::kScaleAt) + kept * (2 * kBlock * 4);
                     vd = kd + kBlock * 4;
-                    ev = sh.exponent[kept];
-                    int e = ev[0];
+                    over = sh.kept[kept];
+                    const int *ev = sh.exponent[kept];
 #pragma unroll
-                    for (int w = 1; w < 4; ++w) e = ev[w] > e ? ev[w] : e;
-                    if (e > ve) {
-                        vfix = exp2_fast(static_cast<float>(ve - e));
-                        ve = e;
-                    }
+                    for (int w = 0; w < 4; ++w) e_block = ev[w] > e_block ? ev[w] : e_block;
                     // a scale that is not finite makes the rows that see its place NaN
 #pragma unroll 1
                     for (int w = 0; w < 4; ++w) {
@@ -861,14 +893,14 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                                 top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale;
                             } else {
                                 // Weights carry their 32 places' power of two, 2^(e - ve), in the
-                                // exponent (not below 2^-40: such values are lost in the others'
-                                // rounding), and the sum is taken without it.
+                                // exponent (not below 2^-100: such weights are 0 as fp16 either
+                                // way), and the sum is taken without it.
                                 l_half = 0.0f;
                                 float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                                 for (int g = 0; g < 2; ++g) {
-                                    const int drop = ev[2 * h + g] - ve;
-                                    const float by = drop < -40 ? -40.0f : static_cast<float>(drop);
+                                    const int drop = over[2 * h + g] - ve;
+                                    const float by = drop < -100 ? -100.0f : static_cast<float>(drop);
                                     const uint64_t c2 = pair(c0 + by, c0 + by);
                                     float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                                     uint64_t sum[2] = {0ull, 0ull};
@@ -897,7 +929,20 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                                 top = fmaxf(t[0], t[1]);
                             }
                             const bool rises = top > m + kLazy;   // (no maximum yet: -inf + 5 < any score)
-                            if (!__any_sync(0xffffffffu, rises) && vfix == 1.0f) break;
+                            if (!__any_sync(0xffffffffu, rises || e_block > ve)) break;
+                            float vfix = 1.0f;
+                            if (KIND == kKvQ8 && e_block > ve) {
+                                // As far as this row sees them.  (In this branch, which a block seldom
+                                // takes, and not ahead of the block's halves, where it made every
+                                // block of 8-bit rows 4 to 20 % slower.)
+                                int e = e_block > kMostExponent ? kMostExponent : e_block;
+                                if (masked)
+                                    e = seen_exponent(vd, smem_u32(over), e, tree_row, p.tree_words, node, seg.w.nodes, len, j0, ve);
+                                vfix = exp2_fast(static_cast<float>(ve - e));
+                                ve = e;
+                                e_block = kLeastExponent;
+                            }
+                            __syncwarp();
                             if (!first) {
                                 // of the products before these weights only the last may still run
                                 ok = warp_wait_or_give_up(&b.o_full[x][1 - h], h == 1 ? ns : ns ^ 1u, gave_up, p.status);
@@ -917,7 +962,6 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                                 }
                             }
                             if (rises) m = top;
-                            vfix = 1.0f;
                         }
                         if (!ok) break;
                         if constexpr (KIND == kKvF16) st_32cols(s_at + 64 * h, w);
@@ -985,7 +1029,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                 if (x == 1) {
                     sh.m[wt] = m;
                     sh.l[wt] = l;
-                    if (wt == 0) sh.ve = ve;
+                    sh.ve[wt] = ve;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
@@ -1019,7 +1063,7 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                     m = top;
                     if constexpr (KIND == kKvQ8) {
                         f *= power_of_2(ve);
-                        f1 *= power_of_2(sh.ve);
+                        f1 *= power_of_2(sh.ve[wt]);
                     }
                 }
                 const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
