@@ -396,7 +396,11 @@ QMV_API qmv_status qmm_q8_0_prefill(const void *W, const void *x, float *y,
  *   len + number of nodes its row names - 1, not below len) and request.
  *   Places of the T token outputs past the last new token get slot -1, pos 0
  *   and request -1.
- * Calling it again with the same inputs gives the same outputs.
+ * Calling it again with the same inputs gives the same outputs.  No output may
+ * be an input's memory (table apart).
+ * What a request holds follows from its length alone: one whose length is cut
+ * back (rejected tokens) first gives its pages past ceil(len / page) back to
+ * the list, or the program counts its pages, with qmv_kv_pages_held.
  * More than T new tokens: the ones past T are dropped (start and kv_len count
  * the rest).  A list or table row that is too short: the slots without a page
  * are -1, and so are the table entries.  Both set QMV_DEV_NO_PAGES.  A page id
@@ -409,6 +413,25 @@ QMV_API qmv_status qmv_kv_pages(const int32_t *len, const int32_t *n_new, const 
                         int32_t *table, int32_t *start, int32_t *kv_len, int32_t *slots, int32_t *pos,
                         int32_t *request, int32_t *head_out, int64_t R, int64_t width, int64_t page,
                         int64_t n_pages, int64_t T, qmv_stream_t stream);
+
+/*
+ * qmv_kv_pages for requests that may hold more pages than their length fills:
+ * a step's rejected tokens are taken off `len`, and their pages stay where they
+ * are for the next ones.
+ *   held     : int32 [R], pages of each request; with need = ceil(len / page),
+ *              entries [0, max(held, need)) of its row are read and kept, and
+ *              only those past them are filled from the list.  NULL: need.
+ *   held_out : int32 [R] (may be NULL), the pages each holds after the step;
+ *              entries that the list had no page for do not count, and none is
+ *              taken for tokens past the end of the row.
+ * A count below 0 or above width sets QMV_DEV_BAD_LENGTH and is taken as the
+ * nearer of the two.  All else as for qmv_kv_pages.
+ */
+QMV_API qmv_status qmv_kv_pages_held(const int32_t *len, const int32_t *n_new, const int32_t *free_pages,
+                             int64_t n_free, const int32_t *head, const int32_t *tree, int64_t tree_words,
+                             int32_t *table, const int32_t *held, int32_t *start, int32_t *kv_len, int32_t *slots,
+                             int32_t *pos, int32_t *request, int32_t *head_out, int32_t *held_out, int64_t R,
+                             int64_t width, int64_t page, int64_t n_pages, int64_t T, qmv_stream_t stream);
 
 /*
  * Writes the key and value rows of T new tokens into the cache, rotated by

@@ -20,6 +20,7 @@ Functions (same names as the C ABI):
     qmm_q8_0_prefill(W, x, y=None, stream=None)  -> y fp32 [M, N]
     KvCache(k, v, k_scale=None, v_scale=None), qmv_kv_cache(...) -> a paged key/value cache (fp16 or int8 rows)
     qmv_kv_pages(lens, n_new, free, table, page, tokens, ...) -> KvPages: start, kv_len, slots, pos, request, head
+                                                                (with held=...: KvPagesHeld, and held)
     qmv_kv_append(qkv, cache, slots, n_heads, pos, cos, sin, ...) -> rotated q; k, v rows written to the cache
     qmv_tree_attn(q, cache, table, start, kv_len, tree=None, ...) -> attention over the cache, fp16 [T, heads, D]
     qmv_tree_attn_workspace(device=None)         -> the workspace a program keeps for qmv_tree_attn
@@ -97,6 +98,8 @@ def lib():
         ci = ctypes.c_int
         L.qmv_kv_pages.restype = ci
         L.qmv_kv_pages.argtypes = [vp, vp, vp, i64, vp, vp, i64] + [vp] * 7 + [i64] * 5 + [vp]
+        L.qmv_kv_pages_held.restype = ci
+        L.qmv_kv_pages_held.argtypes = [vp, vp, vp, i64, vp, vp, i64] + [vp] * 9 + [i64] * 5 + [vp]
         L.qmv_kv_append.restype = ci
         L.qmv_kv_append.argtypes = [vp, i64, ci, vp, vp, vp, vp, i64, i64, ci, vp, vp, vp, vp, vp, ci] + [i64] * 7 + [vp]
         L.qmv_tree_attn_workspace.restype = i64
@@ -539,6 +542,17 @@ class KvPages(NamedTuple):
     head: object       # [1] index in the free list after the last page taken
 
 
+class KvPagesHeld(NamedTuple):
+    """KvPages, and what each request holds after the step (qmv_kv_pages with `held`)."""
+    start: object
+    kv_len: object
+    slots: object
+    pos: object
+    request: object
+    head: object
+    held: object       # [R] pages of each request, also past its length
+
+
 # The paged-cache calls take a few microseconds on the GPU, so their checks look at each property of a tensor once
 # (get_device: the index, or -1 for a CPU tensor).
 
@@ -609,11 +623,13 @@ def _output(shape, dtype, device, index, stream):
     return out
 
 
-def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n_pages=None, stream=None):
+def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n_pages=None, stream=None, held=None):
     """Page and slot maps of one step, on the GPU.  lens, n_new [R]; free [n], ids of unused pages, taken in order
     from index `head` ([1], default 0) on; table [R, width] is completed in place; tokens: length of the per-token
     outputs (what the new tokens leave over is padding); tree [tokens, words]: positions are depths.  n_pages: size
-    of the cache, to refuse wrong page ids (default: any that a slot can hold).  Returns KvPages."""
+    of the cache, to refuse wrong page ids (default: any that a slot can hold).  held [R]: pages that each request
+    holds, where rejected tokens were taken off its length and their pages stay (default: what its length fills, so a
+    program that cuts a length back returns the pages past it to the list).  Returns KvPages, with `held` KvPagesHeld."""
     torch = _torch()
     fn = "qmv_kv_pages"
     at = lens.get_device()
@@ -630,16 +646,27 @@ def qmv_kv_pages(lens, n_new, free, table, page, tokens, head=None, tree=None, n
         if head.shape[0] != 1:
             raise ValueError(f"{fn}: head must be one number")
     tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, tokens, at)
-    size = 2 * R + 2 + 3 * tokens
+    held_ptr = 0
+    if held is not None:
+        held_ptr = _int32(fn, "held", held, 1, at)
+        if held.shape[0] != R:
+            raise ValueError(f"{fn}: held must have one number to a request")
+    size = 2 * R + 2 + 3 * tokens + (0 if held is None else R)
     out = torch.empty(size, dtype=torch.int32, device=lens.device) if stream is None else \
         _output(size, torch.int32, lens.device, at, stream)
     o, n = out.data_ptr(), 4 * tokens
     s = o + 4 * (2 * R + 1)
-    _call_on(fn, at, stream,
-             (len_ptr, new_ptr, free_ptr, free.shape[0], head_ptr, tree_ptr, words, table_ptr, o, o + 4 * (R + 1), s,
-              s + n, s + 2 * n, s + 3 * n, R, table.shape[1], page,
+    if held is None:
+        _call_on(fn, at, stream,
+                 (len_ptr, new_ptr, free_ptr, free.shape[0], head_ptr, tree_ptr, words, table_ptr, o, o + 4 * (R + 1), s,
+                  s + n, s + 2 * n, s + 3 * n, R, table.shape[1], page,
+                  (0x7fffffff // page) if n_pages is None else int(n_pages), tokens))
+        return KvPages(*out.split_with_sizes((R + 1, R, tokens, tokens, tokens, 1)))
+    _call_on("qmv_kv_pages_held", at, stream,
+             (len_ptr, new_ptr, free_ptr, free.shape[0], head_ptr, tree_ptr, words, table_ptr, held_ptr, o,
+              o + 4 * (R + 1), s, s + n, s + 2 * n, s + 3 * n, s + 3 * n + 4, R, table.shape[1], page,
               (0x7fffffff // page) if n_pages is None else int(n_pages), tokens))
-    return KvPages(*out.split_with_sizes((R + 1, R, tokens, tokens, tokens, 1)))
+    return KvPagesHeld(*out.split_with_sizes((R + 1, R, tokens, tokens, tokens, 1, R)))
 
 
 def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, interleaved=False, q=None, stream=None):

@@ -13,7 +13,7 @@ namespace {
 // ---- page and slot maps -------------------------------------------------------
 //
 //   start[r]  = sum over s < r of n[s]
-//   have, need = ceil(len / page), ceil((len + n) / page) per request
+//   have, need = ceil(len / page) or the pages it holds, if more; ceil((len + n) / page) per request
 //   table[r][have .. need) = free[head + sum over s < r of (need - have) ..]
 //   slot of request r's i-th new token = table[r][(len + i) / page] * page + (len + i) % page
 //   pos  = len + i, or with a tree mask len + (nodes its row sees) - 1: its depth
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesPara
     int bad = head < 0 || head > p.n_free ? kDevNoPages : 0;
     for (int64_t r0 = 0; r0 < p.R; r0 += kPagesThreads) {
         const int n = static_cast<int>(p.R - r0 < kPagesThreads ? p.R - r0 : kPagesThreads);
-        int64_t len = 0, fresh = 0, cnt = 0;
+        int64_t len = 0, fresh = 0, cnt = 0, hold = 0;
         if (tid < n) {
             len = p.len[r0 + tid];
             cnt = p.n_new[r0 + tid];
@@ -109,6 +109,13 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesPara
                 bad |= kDevBadLength;
                 len = len < 0 ? 0 : len;
                 cnt = 0;
+            }
+            if (p.held) {
+                hold = p.held[r0 + tid];
+                if (hold < 0 || hold > p.width) {
+                    bad |= kDevBadLength;
+                    hold = hold < 0 ? 0 : p.width;
+                }
             }
         }
         // Tokens past T are dropped: the counts are cut so that the offsets end at T.
@@ -120,8 +127,11 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesPara
             bad |= kDevNoPages;
             cnt = p.T - first;
         }
-        const int64_t have = (len + page - 1) >> p.page_shift;
-        if (tid < n) fresh = ((len + cnt + page - 1) >> p.page_shift) - have;
+        int64_t have = (len + page - 1) >> p.page_shift;
+        if (have < hold) have = hold;
+        int64_t need = (len + cnt + page - 1) >> p.page_shift;
+        if (p.held && need > p.width) need = p.width;   // no page is taken that the row has no entry for
+        if (tid < n && need > have) fresh = need - have;
         int64_t last = first + cnt, upto = fresh;
         __syncthreads();   // warp_sums again
         none = 0;
@@ -142,6 +152,10 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesPara
             if (tid < n) {
                 p.start[r0 + tid] = static_cast<int32_t>(first);
                 p.kv_len[r0 + tid] = static_cast<int32_t>(len + cnt);
+                if (p.held_out) {   // with the fresh pages that the list had
+                    const int64_t left = p.n_free - base, got = base < 0 || left < 0 ? 0 : (fresh < left ? fresh : left);
+                    p.held_out[r0 + tid] = static_cast<int32_t>(have + got < p.width ? have + got : p.width);
+                }
                 if (r0 + tid == p.R - 1) {
                     p.start[p.R] = static_cast<int32_t>(last);
                     if (p.head_out)

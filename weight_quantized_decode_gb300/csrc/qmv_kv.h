@@ -22,8 +22,8 @@ constexpr int kKvF16 = 0;
 constexpr int kKvQ8 = 1;
 
 struct PagesParams {
-    const int32_t *len, *n_new, *free_pages, *head, *tree;
-    int32_t *table, *start, *kv_len, *slots, *pos, *request, *head_out;
+    const int32_t *len, *n_new, *free_pages, *head, *tree, *held;
+    int32_t *table, *start, *kv_len, *slots, *pos, *request, *head_out, *held_out;
     int64_t n_free, R, width, T;
     int tree_words, page_shift;
     int64_t n_pages;

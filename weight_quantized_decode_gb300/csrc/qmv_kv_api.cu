@@ -66,6 +66,16 @@ qmv_status qmv_kv_pages(const int32_t *len, const int32_t *n_new, const int32_t 
                         int32_t *head_out, int64_t R, int64_t width, int64_t page, int64_t n_pages, int64_t T,
                         qmv_stream_t stream)
 {
+    return qmv_kv_pages_held(len, n_new, free_pages, n_free, head, tree, tree_words, table, nullptr, start, kv_len, slots,
+                             pos, request, head_out, nullptr, R, width, page, n_pages, T, stream);
+}
+
+qmv_status qmv_kv_pages_held(const int32_t *len, const int32_t *n_new, const int32_t *free_pages, int64_t n_free,
+                             const int32_t *head, const int32_t *tree, int64_t tree_words, int32_t *table,
+                             const int32_t *held, int32_t *start, int32_t *kv_len, int32_t *slots, int32_t *pos,
+                             int32_t *request, int32_t *head_out, int32_t *held_out, int64_t R, int64_t width,
+                             int64_t page, int64_t n_pages, int64_t T, qmv_stream_t stream)
+{
     const int shift = page_shift_of(page);
     if (shift < 0 || R < 0 || R > kInt32Max || width < 0 || width > kInt32Max || T < 0 || T > kInt32Max ||
         n_free < 0 || n_free > kInt32Max || n_pages < 1 || n_pages > kInt32Max / page || tree_words < 0 ||
@@ -80,7 +90,8 @@ qmv_status qmv_kv_pages(const int32_t *len, const int32_t *n_new, const int32_t 
                           static_cast<const void *>(tree), static_cast<const void *>(table),
                           static_cast<const void *>(start), static_cast<const void *>(kv_len),
                           static_cast<const void *>(slots), static_cast<const void *>(pos),
-                          static_cast<const void *>(request), static_cast<const void *>(head_out)})
+                          static_cast<const void *>(request), static_cast<const void *>(head_out),
+                          static_cast<const void *>(held), static_cast<const void *>(held_out)})
         if (!aligned(p, 4)) return QMV_ERR_ALIGN;
     PagesParams p = {};
     int sms = 0;
@@ -98,6 +109,8 @@ qmv_status qmv_kv_pages(const int32_t *len, const int32_t *n_new, const int32_t 
     p.pos = pos;
     p.request = request;
     p.head_out = head_out;
+    p.held = held;
+    p.held_out = held_out;
     p.n_free = n_free;
     p.R = R;
     p.width = width;

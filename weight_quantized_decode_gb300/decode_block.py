@@ -34,6 +34,7 @@ class AttentionBlock:
         self.lens = torch.zeros(requests, **i32)
         self.free = torch.randperm(n_pages, device="cuda").to(torch.int32)
         self.head = torch.zeros(1, **i32)
+        self.held = torch.zeros(requests, **i32)      # pages of each request, also past its length
         turn = base ** (-torch.arange(0, head_dim, 2, dtype=torch.float64, device="cuda") / head_dim)
         angle = torch.arange(positions, dtype=torch.float64, device="cuda")[:, None] * turn
         self.cos, self.sin = angle.cos().float(), angle.sin().float()
@@ -48,16 +49,16 @@ class AttentionBlock:
         T = x.shape[0]
         qkv = self._product(self.Wqkv, x)
         maps = qmv.qmv_kv_pages(self.lens, n_new, self.free, self.table, self.page, T, head=self.head, tree=tree,
-                                n_pages=self.cache.n_pages)
+                                n_pages=self.cache.n_pages, held=self.held)
         q = qmv.qmv_kv_append(qkv, self.cache, maps.slots, self.heads, pos=maps.pos, cos=self.cos, sin=self.sin)
         a = qmv.qmv_tree_attn(q, self.cache, self.table, maps.start, maps.kv_len, tree=tree, workspace=self.work)
         y = self._product(self.Wo, a.view(T, -1))
-        self.lens, self.head = maps.kv_len, maps.head
+        self.lens, self.head, self.held = maps.kv_len, maps.head, maps.held
         return y, maps
 
     def keep(self, request, maps, path):
         """After a tree step: of `request`'s new tokens only the nodes of `path` (indices, root first) stay, in that
-        order, and its length ends behind them.  Their pages stay with the request."""
+        order, and its length ends behind them.  The others' pages stay with the request (`held`), for its next tokens."""
         torch, page = self.torch, self.page
         start = int(maps.start[request])
         slots = maps.slots[start:int(maps.start[request + 1])].long()
@@ -110,12 +111,12 @@ def main() -> int:
         bad = qmv.qmv_device_status()
         # a captured tree step
         block = tree
-        state = block.lens, block.head
+        state = block.lens, block.head, block.held
         side = torch.cuda.Stream()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.stream(side):
             block.step(x[prompt:-1], one(len(parents)), tree=mask)
-            block.lens, block.head = state
+            block.lens, block.head, block.held = state
             n_new = one(len(parents))
             side.synchronize()
             with torch.cuda.graph(graph, stream=side):
