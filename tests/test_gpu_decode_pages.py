@@ -121,3 +121,20 @@ def test_held_counts_pages_that_there_were(q):
         q.qmv_kv_pages(lens, news, dev([1]), dev(table), 16, 100, held=dev([1]))
     with pytest.raises(TypeError):
         q.qmv_kv_pages(lens, news, dev([1]), dev(table), 16, 100, held=dev([1, 1]).float())
+
+
+def test_nothing_is_kept_of_a_step_without_pages(q):
+    """A step whose free list ran out left tokens without a slot: keep refuses, and no
+    row of the cache changes (a slot of -1 would be the last page's last row)."""
+    from weight_quantized_decode_gb300.decode_block import tree_mask
+    block, hidden = small_block(1, 2, 4, 16)
+    mask = torch.from_numpy(tree_mask([-1, 0, 0, 2])).cuda()
+    x = torch.randn(31, hidden, device="cuda").half()
+    block.step(x, dev([31]))
+    _, maps = block.step(x[:4], dev([4]), tree=mask)
+    assert (maps.slots < 0).any() and q.qmv_device_status() != 0
+    before = block.cache.k.clone(), block.cache.v.clone(), block.lens.clone()
+    with pytest.raises(RuntimeError):
+        block.keep(0, maps, [0, 2, 3])
+    for a, b in zip(before, (block.cache.k, block.cache.v, block.lens)):
+        assert torch.equal(a, b)

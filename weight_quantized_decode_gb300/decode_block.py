@@ -62,6 +62,8 @@ class AttentionBlock:
         torch, page = self.torch, self.page
         start = int(maps.start[request])
         slots = maps.slots[start:int(maps.start[request + 1])].long()
+        if bool((slots < 0).any()):
+            raise RuntimeError("keep: the step had no pages for some of the request's tokens; nothing of it can be kept")
         frm, to = slots[torch.as_tensor(path, device="cuda")], slots[:len(path)]
         for pool in (self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale):
             if pool is not None:
