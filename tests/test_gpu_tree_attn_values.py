@@ -110,3 +110,28 @@ def test_large_value_scales_of_unseen_nodes(q, ws, ctx, heads, D, T, tree, big):
         got = call(q, p, ws).cpu().numpy().astype(np.float64)
         assert np.all(np.abs(got[off] - want[off]) <= allow[off]), (node, np.nanmax(np.abs(got[off] - want[off])))
     assert q.qmv_device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("heads,D,T", ROWS)
+@pytest.mark.parametrize("ctx", [0, 50, 9000])
+def test_a_seen_value_that_is_not_finite_shows_whatever_its_weight(q, ws, ctx, heads, D, T, bad):
+    """fp16 rows: infinity or NaN times a weight too small for fp16 or fp32 is
+    still not a finite number."""
+    prob = ref.problem([ctx], [T], heads, 1, D, 16, seed=T)
+    one = prob["q"][0, 0].copy()
+    prob["q"][:] = one
+    unit = one.astype(np.float64) / np.linalg.norm(one.astype(np.float64))
+    far = -100.0 / (np.linalg.norm(one.astype(np.float64)) * D ** -0.5)      # a score of -100
+    for low in (1, ctx + T - 1):        # node 1 alone, then all but the first place
+        p = copy(prob)
+        node = 1
+        for j in range(ctx + T - low if low > 1 else ctx + node, ctx + T if low > 1 else ctx + node + 1):
+            p["k"][p["table"][0, j // 16], 0, j % 16] = (unit * far).astype(np.float16)
+        at = ctx + node
+        p["v"][p["table"][0, at // 16], 0, at % 16, 5] = bad
+        got = call(q, p, ws).cpu().numpy().astype(np.float64)
+        on = seeing(p, node, T)
+        assert not np.isfinite(got[on][:, :, 5]).any(), low
+        assert np.isfinite(got[~on]).all()
+    assert q.qmv_device_status() == 0

@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             release(2 * s);
             // ---- places a row does not see ----
             uint32_t see[NR][2];   // of rows 8 n + 2 t4, + 1; shifted so that bit 0 is place g
+            uint32_t mine = 0u;    // of row `lane`
             if (masked) {
-                uint32_t mine = 0u;
                 if (lane < valid) {
                     const int node = static_cast<int>((row_base + lane) / group_size);
                     mine = seen_places(p.tree ? p.tree + (first_token + node) * p.tree_words : nullptr, p.tree_words,
@@ -484,10 +484,10 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
             const uint32_t vb = wait_entry();
             float vfix = 1.0f;
             if constexpr (KIND == kKvQ8) {
-                float mine = lds1(scales_at + 4 * (slot * kStep + lane));
-                if (masked && j0 + lane >= len) mine = 0.0f;
+                float d = lds1(scales_at + 4 * (slot * kStep + lane));
+                if (masked && j0 + lane >= len) d = 0.0f;
                 // largest finite scale of the step; a non-finite one makes its own weights non-finite
-                const int e = exponent_above(__reduce_max_sync(0xffffffffu, finite_bits(mine)));
+                const int e = exponent_above(__reduce_max_sync(0xffffffffu, finite_bits(d)));
                 if (e > ve && !masked) {
                     vfix = exp2_fast(static_cast<float>(ve - e));
                     ve = e;
@@ -634,8 +634,9 @@ __global__ void __launch_bounds__(kThreads, Ring<D, KIND, NR>::kCtas)
                             __syncwarp();
                             for (uint32_t left = odd; left; left &= left - 1u) {
                                 const int j = __ffs(left) - 1;
-                                const bool s0 = __half2float(pscr[2 * t4 * 34 + j]) > 0.0f;
-                                const bool s1 = __half2float(pscr[(2 * t4 + 1) * 34 + j]) > 0.0f;
+                                // (a weight of 0 counts as well: seen infinities and NaN show)
+                                const bool s0 = __shfl_sync(0xffffffffu, mine, 8 * n + 2 * t4) >> j & 1u;
+                                const bool s1 = __shfl_sync(0xffffffffu, mine, 8 * n + 2 * t4 + 1) >> j & 1u;
                                 const float w0 = __half2float(pscr[2 * t4 * 34 + j]);
                                 const float w1 = __half2float(pscr[(2 * t4 + 1) * 34 + j]);
 #pragma unroll

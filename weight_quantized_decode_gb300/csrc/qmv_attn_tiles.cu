@@ -1053,9 +1053,12 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
             float *part = whole ? nullptr : workspace_partial(p, blockIdx.x, seg.b0 == 0 ? 1 : 0, kRows, D);
             if (two || x == 0) {
                 float f1 = 0.0f;
+                bool own = !first, other = false;  // outputs of this stream, and of stream 1, are to be added
                 if (KIND == kKvQ8 && two) f = power_of_2(ve);
                 if (!two) {
                     const float m1 = sh.m[wt], top = fmaxf(m, m1);
+                    own = own && m != -INFINITY;   // (also those whose factor is 0: infinities and NaN show)
+                    other = m1 != -INFINITY;
                     f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
                     f1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
                     const float l1 = sh.l[wt];
@@ -1086,8 +1089,8 @@ __global__ void __launch_bounds__(Ring<D, KIND>::kThreads, 1)
                     }
                     if (row >= valid) continue;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = first || f == 0.0f ? 0.0f : __uint_as_float(v[k]) * f;
-                    if (!two && f1 != 0.0f) {
+                    for (int k = 0; k < 32; ++k) o[k] = own ? __uint_as_float(v[k]) * f : 0.0f;
+                    if (other) {
                         const float *xo = reinterpret_cast<const float *>(qbuf) + wt * D;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
