@@ -450,7 +450,8 @@ QMV_API qmv_status qmv_kv_pages_held(const int32_t *len, const int32_t *n_new, c
  *   pos, cos_table, sin_table : int32 [T], fp32 [n_pos][rot / 2].
  *   q     : fp16 [T][Hq][D], rounded once.  k, v: see the cache layout.
  * An 8-bit row is d = max |y| / 127 (fp32) and codes round(y / d), ties away
- * from zero (y times the rounded reciprocal of d); rows must be finite.
+ * from zero (y times the rounded reciprocal of d).  A row with an infinity or
+ * NaN gets a scale that is not finite (a token that sees it, NaN).
  * A slot outside the cache other than -1 writes nothing (QMV_DEV_BAD_PAGE); a
  * position outside [0, n_pos) gives a NaN query row and no cache row
  * (QMV_DEV_BAD_LENGTH).

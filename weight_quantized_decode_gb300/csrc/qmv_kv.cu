@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesPara
 // For each token: its query heads, rotated, as fp16 to q; its key heads,
 // rotated, and its value heads to the cache row of its slot, as fp16 or as
 // 8-bit codes with one fp32 scale d = max |y| / 127 to the row,
-// code = round(y / d).  A rotation of pair (a, b) by the position's (cos, sin)
+// code = round(y / d); a row that is not finite has a scale that is not, and codes of
+// 0.  A rotation of pair (a, b) by the position's (cos, sin)
 // is (a cos - b sin, b cos + a sin); products and sums are rounded one by one
 // in fp32, so that a code does not depend on how a compiler fuses them.
 //
@@ -353,10 +354,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
                     *reinterpret_cast<uint2 *>(static_cast<__half *>(is_v ? p.v : p.k) + cell * p.page_stride +
                                                in_page * D + 4 * g) = packed;
             } else {
-                float amax = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+                // largest magnitude, by its bits: NaN counts as larger than any number
+                uint32_t most = 0u;
 #pragma unroll
-                for (int d = 1; d < G; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-                const float d = __fdiv_rn(amax, 127.0f);
+                for (int j = 0; j < 4; ++j) most = max(most, __float_as_uint(y[j]) & 0x7fffffffu);
+#pragma unroll
+                for (int d = 1; d < G; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+                const float d = __fdiv_rn(__uint_as_float(most), 127.0f);
                 // (a row whose largest value is below 2^-119 is stored as zeros: 1 / d would overflow)
                 const float id = d >= 1.17549435e-38f ? __frcp_rn(d) : 0.0f;
                 uint32_t word = 0u;
