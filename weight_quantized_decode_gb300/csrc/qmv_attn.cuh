@@ -28,6 +28,16 @@
 
 namespace qmv {
 
+// How each kernel cuts its work: rows of a unit (for few rows: 8, 16 or 32), places of a
+// block, and what a unit costs besides its blocks, in blocks (tiles: 3 .. 6 measured
+// within 3 %).  Stated here for the kernels and for the check of the split alike.
+struct RowsSplit {
+    static constexpr int kBlock = 128, kCost = 2;
+};
+struct TilesSplit {
+    static constexpr int kRows = 256, kBlock = 128, kCost = 5;
+};
+
 // a / b for a, b >= 0, in 32 bits where they fit (a 64-bit division is a long
 // sequence of dependent instructions).
 __host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)

@@ -37,10 +37,10 @@ namespace qmv {
 
 namespace {
 
-constexpr int kBlock = 128;
+constexpr int kBlock = RowsSplit::kBlock;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCost = 2;            // what a unit costs besides its blocks, in blocks
+constexpr int kCost = RowsSplit::kCost;
 constexpr int kStep = 32;           // places of a warp's step
 constexpr float kShift = 10.0f;     // weights are 2^10 times exp(s - max)
 

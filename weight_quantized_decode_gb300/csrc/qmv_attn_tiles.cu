@@ -53,9 +53,10 @@ namespace qmv {
 namespace {
 
 constexpr int kTile = 128;           // rows of a stream
-constexpr int kRows = 2 * kTile;     // rows of a unit
-constexpr int kBlock = 128;          // places of a block
-constexpr int kCost = 5;             // what a unit costs besides its blocks, in blocks (3 .. 6: within 3 %)
+constexpr int kRows = TilesSplit::kRows;
+constexpr int kBlock = TilesSplit::kBlock;
+constexpr int kCost = TilesSplit::kCost;
+static_assert(kRows == 2 * kTile && kBlock == kTile, "two streams of a tile, and a thread of each to a place");
 constexpr int kMmaWarp = 8, kCopyWarp = 9;   // and 10: the second stream's products
 constexpr int kQueryWarp = 11;
 constexpr int kExpandWarp = 12;      // 12-15, for 8-bit rows only
