@@ -496,8 +496,9 @@ class KvCache:
         if k.dim() != 4 or k.shape != v.shape or k.device != v.device:
             raise ValueError("KvCache: k and v must be [n_pages, kv_heads, page, head_dim] on one device")
         n_pages, heads, page, dim = k.shape
-        dense = (page * dim, dim, 1)
-        if tuple(k.stride()[1:]) != dense or tuple(v.stride()[1:]) != dense or (n_pages > 1 and k.stride(0) != v.stride(0)):
+        # (one head's stride means nothing: a pool [n_pages, page, 1, head_dim] transposed will do)
+        dense = all(tuple(t.stride()[2:]) == (dim, 1) and (heads == 1 or t.stride(1) == page * dim) for t in (k, v))
+        if not dense or (n_pages > 1 and k.stride(0) != v.stride(0)):
             raise ValueError("KvCache: the rows of a page must be dense, and k and v have one page stride")
         kind = QMV_KV_F16 if k.dtype == torch.float16 else QMV_KV_Q8
         for s in (k_scale, v_scale):
