@@ -486,9 +486,14 @@ QMV_API int64_t qmv_tree_attn_workspace(void);
  * times their value scale) enter the value product rounded to fp16, of which
  * half a subnormal step is 2^-35 of the largest weight's (8-bit rows: times the
  * largest value scale that the token sees); the output is rounded once.
- * Rows of `out` past start[R] are left as they are.  A request whose page ids
- * leave [0, n_pages), or whose kv_len is below its new tokens or above
- * width * page, gets NaN (QMV_DEV_BAD_PAGE); other requests are unaffected.
+ * Rows of `out` past start[R] are left as they are.  A request whose kv_len is
+ * below its new tokens or above width * page gets NaN; where a page id of its
+ * first ceil(kv_len / page) leaves [0, n_pages), so do the tokens that may see a
+ * place of that page (its other tokens get NaN or their values).  Both set
+ * QMV_DEV_BAD_PAGE; other requests are unaffected.
+ * One kernel takes all requests of a call, chosen by their average number of new
+ * tokens: a batch of single tokens and chunks of prompts is best made two calls,
+ * one for each kind (1.1 to 2.6 times as fast, measured).
  * Hq a multiple of Hkv, 0 <= R <= 2^20, 0 <= T <= 2^24, T * Hq < 2^31.
  */
 QMV_API qmv_status qmv_tree_attn(const void *q, int64_t q_stride, const void *k, const void *v,

@@ -56,12 +56,29 @@ int64_t tree_attn_workspace_bytes(int sms)
 
 cudaError_t launch_tree_attn(const AttnParams &p, int D, int kind, int sms, cudaStream_t s, bool pdl)
 {
-    // Rows that share a key/value head in the average request: up to 32 are one
-    // unit of the streaming kernel; more go to the 128-row tiles.  Measured, 32
-    // heads on 8 of 128, streaming against tiles: one request of 30001 places,
-    // 32 rows 36 against 39 us, 48 rows 44 against 42, 128 rows 71 against 50;
-    // 16 requests of 4000, 32 rows 57 against 61, 48 rows 85 against 65; 8-bit
-    // rows the same way (32 rows 57 against 89, 48 rows 98 against 89).
+    // Rows that share a key/value head in the average request (of T / R tokens,
+    // padding included): up to 32 are one unit of the streaming kernel; more go to
+    // the 128-row tiles.  Measured, us, streaming kernel against tiles:
+    //   heads of         32 on 8 of 128               64 on 8 of 64
+    //   fp16, 1 request of 30001 places
+    //     32 rows         36.6     39.2                25.0     26.6
+    //     48 rows         43.4     43.0                31.5     27.9
+    //   fp16, 16 requests of 4000
+    //     32 rows         56.4     62.1                35.8     41.5
+    //     48 rows         84.7     64.8                58.6     43.1
+    //   8-bit, 1 request of 30001
+    //     32 rows         35.9     40.0                25.6     34.0
+    //     48 rows         51.0     41.6                36.9     34.6
+    //   8-bit, 16 requests of 4000
+    //     32 rows         57.2     86.1                41.1     62.0
+    //     48 rows         97.7     88.3                70.3     63.4
+    // The average says nothing of a batch that mixes single tokens and chunks of
+    // prompts, and one kernel then takes both: 127 single tokens over 4096 places
+    // and 512 tokens behind 8192, 559 us (8-bit 690) on the kernel chosen, 465 (829)
+    // on the other, as two calls 316 + 79 (184 + 111); 63 and 1500 tokens 282 (493),
+    // 581 (656), as two calls 165 + 85 (99 + 127).  A choice for each request would
+    // have to be made on the device, where the lengths are; it is not built, and
+    // include/qmv.h tells callers to make two calls.
     const int64_t rows = (p.T + p.R - 1) / p.R * p.group;
     if (rows <= 32) return launch_attn_rows(p, D, kind, rows, sms, s, pdl);
     return launch_attn_tiles(p, D, kind, sms, s, pdl);

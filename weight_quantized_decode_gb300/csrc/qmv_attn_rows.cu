@@ -22,12 +22,16 @@
 // see the same places; from the first step on where some see a larger scale than
 // before and others may not, each row has its own, in shared memory (the last steps
 // of a request; in registers for every step: 60 for 56 us, 16 requests with 32 rows).
+//   Weights are rounded to fp16 for the value product (fp16 x fp16 with fp32
+// accumulators; a wider type would take twice the matrix instructions or more):
+// with fp16 outputs, whose own rounding is 2.1e-4 of the result, that makes 2.4e-4
+// to 2.9e-4.  Scores, maxima, sums, outputs and parts are fp32.
 //   Measured: 64 requests of 100 to 16383 8-bit places, one token of 32 heads on
-// 8 of 128: 185 us, 6.1 TB/s, 0.90 of the measured copy bandwidth; 16 uneven
+// 8 of 128: 186 us, 6.1 TB/s, 0.90 of the measured copy bandwidth; 16 uneven
 // trees of up to 24 nodes over 511 to 8191 fp16 places, 16 heads on 8: 63 us,
 // 0.68.  One request has little to stream and pays for the start, the ragged
-// end and the join: 8 nodes over 30001 places 35 us where the bytes take 18,
-// one token over 4095 places 9.8 us where they take 2.5.
+// end and the join: 8 nodes over 30001 places 36.5 us where the bytes take 18,
+// one token over 4095 places 10.3 us where they take 2.5.
 #include <cstdint>
 
 #include "qmv_attn.cuh"

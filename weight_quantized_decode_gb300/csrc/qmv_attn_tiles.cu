@@ -25,7 +25,12 @@
 // largest value by each row's running power of two of the largest value scale that
 // the row sees, which enters through the exponent.
 // The scales' arithmetic makes the softmax longer still: the chunks and the eight
-// trees of the figures below take 240 and 138 us, the 16 nodes 190 to 200.
+// trees of the figures below take 234 and 135 us, the 16 nodes 186.
+//   Weights are rounded to fp16 for the value product, as in the kernel for few rows
+// (2.1e-4 of the result from the output's rounding alone, 2.9e-4 with it).
+//   Value rows that no product may see (past the end; nodes' rows that are not finite)
+// are cleared in shared memory by the stream that owns the tile, and in units of more
+// than 128 rows, where both streams read it, by the first for both.
 //   Warps: 0-3 and 4-7 the two softmax groups, 8 and 10 issue their products, 9
 // the copies, 11 brings the next segment's queries as soon as the last products
 // have read this one's (loaded by the softmax groups at a segment's start instead,
@@ -37,9 +42,9 @@
 // its warp (about 850 of arithmetic, the rest waiting for scores to arrive from
 // and weights to arrive in tensor memory), two warps share a scheduler, and the
 // products, 2048 cycles a block of 256 rows at 128 columns, pass beside it (two
-// chunks of 1400 and 1500 tokens behind 2000 and 2800, 32 heads on 8: 151 us,
+// chunks of 1400 and 1500 tokens behind 2000 and 2800, 32 heads on 8: 152 us,
 // 970 TFLOP/s of useful products, 0.51 of the measured bf16 peak; 64 columns:
-// eight trees of 64 nodes over 4001 to 8001 places, 64 heads on 8: 91 us).  A
+// eight trees of 64 nodes over 4001 to 8001 places, 64 heads on 8: 90 us).  A
 // share of the exponentials as polynomials in place of the special-function unit
 // made it slower (a quarter of them: 105 for 91 us), and so did passing a half's
 // weights on only after asking for the next scores (170 for 155).
