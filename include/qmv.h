@@ -588,6 +588,22 @@ QMV_API qmv_status qmv_tree_accept(const int32_t *tokens, const int32_t *sampled
                            qmv_stream_t stream);
 
 /*
+ * qmv_tree_accept for a step in which nodes may have no cache row (a free list that
+ * ran out).
+ *   slots : int32 [T], from qmv_kv_pages: a node whose slot is negative is not
+ *           accepted, nor is one that has no place to be moved to (the slot at
+ *           start[r] + its place in the path is negative).  A request whose first node
+ *           has no slot gets count 0, next -1, a path of -1 and the length it had,
+ *           kv_len - (new tokens).  NULL: every node has a row.
+ * So count, lens and what qmv_kv_keep moves cover the same rows; next is the token
+ * drawn at the last of them.  All else as for qmv_tree_accept.
+ */
+QMV_API qmv_status qmv_tree_accept_slots(const int32_t *tokens, const int32_t *sampled, const int32_t *start,
+                                 const int32_t *kv_len, const int32_t *tree, int64_t tree_words,
+                                 const int32_t *slots, int32_t *path, int32_t *count, int32_t *next, int32_t *lens,
+                                 int64_t R, int64_t T, qmv_stream_t stream);
+
+/*
  * Moves the cache rows of each request's kept nodes to the front of its new places,
  * in `caches` caches (a model's layers) at once: the row at slots[start[r] + path[i]]
  * goes to slots[start[r] + i], i < count[r], for every head, keys and values (and

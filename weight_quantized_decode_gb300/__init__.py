@@ -28,6 +28,7 @@ Functions (same names as the C ABI):
     qmv_tree_attn_workspace(device=None)         -> the workspace a program keeps for qmv_tree_attn
     qmv_sample(logits, u, temperature, top_k, top_p, min_p, ...) -> Sampled: token, prob
     qmv_tree_accept(tokens, sampled, start, kv_len, tree=None) -> TreeAccepted: path, count, next, lens
+                                                                (with slots=...: no node without a cache row)
     qmv_kv_keep(caches, slots, start, path, count) -> the path's rows moved to the front, in every cache
     qmv_device_status(stream=None)               -> int (QMV_DEV_* bits, cleared)
     qmv_read_probe(buf, out=None, stream=None)   -> checksum tensor (read-only bandwidth probe)
@@ -117,6 +118,8 @@ def lib():
         L.qmv_sample.argtypes = [vp, i64, ci, vp, vp, vp, vp, vp, vp, i64, vp, vp, i64, i64, vp]
         L.qmv_tree_accept.restype = ci
         L.qmv_tree_accept.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, i64, vp]
+        L.qmv_tree_accept_slots.restype = ci
+        L.qmv_tree_accept_slots.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, vp]
         L.qmv_kv_keep.restype = ci
         L.qmv_kv_keep.argtypes = [vp, i64, ci, vp, vp, vp, vp] + [i64] * 7 + [vp]
         L.qmv_tree_attn_workspace.restype = i64
@@ -916,11 +919,12 @@ class TreeAccepted(NamedTuple):
     lens: object       # [R] tokens in the cache up to it
 
 
-def qmv_tree_accept(tokens, sampled, start, kv_len, tree=None, stream=None):
+def qmv_tree_accept(tokens, sampled, start, kv_len, tree=None, stream=None, slots=None):
     """The path of each request's drafted tree that the sampled tokens accept: tokens [T], the one at each node; sampled
     [T], the one drawn at it (qmv_sample on its logits); start [R + 1], kv_len [R], tree [T, words] as qmv_tree_attn
     takes them (None: chains).  A request's first node is accepted, and behind an accepted node its lowest child whose
-    token was drawn there.  Returns TreeAccepted."""
+    token was drawn there.  slots [T], from qmv_kv_pages: nodes that got no page (a negative slot) are not accepted, and a
+    request whose first node got none keeps nothing (count 0, next -1, the length it had).  Returns TreeAccepted."""
     torch = _torch()
     fn = "qmv_tree_accept"
     at = tokens.get_device()
@@ -930,12 +934,18 @@ def qmv_tree_accept(tokens, sampled, start, kv_len, tree=None, stream=None):
     if sampled.shape[0] != T or start.shape[0] != R + 1:
         raise ValueError(f"{fn}: tokens and sampled [T], start [R + 1] and kv_len [R] must agree")
     tree_ptr, words = (0, 0) if tree is None else _tree_args(fn, tree, T, at)
+    slots_ptr = 0
+    if slots is not None:
+        slots_ptr = _int32(fn, "slots", slots, 1, at)
+        if slots.shape[0] != T:
+            raise ValueError(f"{fn}: one slot to a token")
     size = T + 3 * R
     out = torch.empty(size, dtype=torch.int32, device=tokens.device) if stream is None else \
         _output(size, torch.int32, tokens.device, at, stream)
     o = out.data_ptr()
     c = o + 4 * T
-    _call_on(fn, at, stream, (tok, drawn, start_ptr, len_ptr, tree_ptr, words, o, c, c + 4 * R, c + 8 * R, R, T))
+    _call_on("qmv_tree_accept_slots", at, stream,
+             (tok, drawn, start_ptr, len_ptr, tree_ptr, words, slots_ptr, o, c, c + 4 * R, c + 8 * R, R, T))
     return TreeAccepted(*out.split_with_sizes((T, R, R, R)))
 
 

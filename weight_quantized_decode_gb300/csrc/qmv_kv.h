@@ -57,6 +57,7 @@ struct NormAppendParams {
 // The accepted path of each request's drafted tree.
 struct AcceptParams {
     const int32_t *tokens, *sampled, *start, *kv_len, *tree;
+    const int32_t *slots;                // [T], negative where a node has no cache row; or null
     int32_t *path, *count, *next, *lens;
     int64_t R, T;
     int tree_words;

@@ -241,9 +241,10 @@ qmv_status qmv_kv_append_norm(const void *qkv, int64_t stride, int qkv_f32, cons
     return QMV_OK;
 }
 
-qmv_status qmv_tree_accept(const int32_t *tokens, const int32_t *sampled, const int32_t *start, const int32_t *kv_len,
-                           const int32_t *tree, int64_t tree_words, int32_t *path, int32_t *count, int32_t *next,
-                           int32_t *lens, int64_t R, int64_t T, qmv_stream_t stream)
+qmv_status qmv_tree_accept_slots(const int32_t *tokens, const int32_t *sampled, const int32_t *start,
+                                 const int32_t *kv_len, const int32_t *tree, int64_t tree_words,
+                                 const int32_t *slots, int32_t *path, int32_t *count, int32_t *next, int32_t *lens,
+                                 int64_t R, int64_t T, qmv_stream_t stream)
 {
     if (R < 0 || R > kInt32Max || T < 0 || T > kInt32Max || tree_words < 0 || tree_words > 65536 ||
         (tree && tree_words == 0))
@@ -251,7 +252,7 @@ qmv_status qmv_tree_accept(const int32_t *tokens, const int32_t *sampled, const 
     if (R == 0 && T == 0) return QMV_OK;
     if ((R > 0 && (!start || !kv_len || !count || !next || !lens)) || (T > 0 && (!tokens || !sampled || !path)))
         return QMV_ERR_NULL;
-    for (const int32_t *a : {tokens, sampled, start, kv_len, tree, static_cast<const int32_t *>(path),
+    for (const int32_t *a : {tokens, sampled, start, kv_len, tree, slots, static_cast<const int32_t *>(path),
                              static_cast<const int32_t *>(count), static_cast<const int32_t *>(next),
                              static_cast<const int32_t *>(lens)})
         if (!aligned(a, 4)) return QMV_ERR_ALIGN;
@@ -264,6 +265,7 @@ qmv_status qmv_tree_accept(const int32_t *tokens, const int32_t *sampled, const 
     p.start = start;
     p.kv_len = kv_len;
     p.tree = tree;
+    p.slots = slots;
     p.path = path;
     p.count = count;
     p.next = next;
@@ -276,6 +278,14 @@ qmv_status qmv_tree_accept(const int32_t *tokens, const int32_t *sampled, const 
         return QMV_ERR_LAUNCH;
     }
     return QMV_OK;
+}
+
+qmv_status qmv_tree_accept(const int32_t *tokens, const int32_t *sampled, const int32_t *start, const int32_t *kv_len,
+                           const int32_t *tree, int64_t tree_words, int32_t *path, int32_t *count, int32_t *next,
+                           int32_t *lens, int64_t R, int64_t T, qmv_stream_t stream)
+{
+    return qmv_tree_accept_slots(tokens, sampled, start, kv_len, tree, tree_words, nullptr, path, count, next, lens, R, T,
+                                 stream);
 }
 
 qmv_status qmv_kv_keep(const void *rows, int64_t caches, int kind, const int32_t *slots, const int32_t *start,

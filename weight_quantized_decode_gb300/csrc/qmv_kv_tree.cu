@@ -13,7 +13,8 @@ namespace {
 // ---- the accepted path ----------------------------------------------------------
 //
 //   node 0 is accepted; behind an accepted node c the lowest j > c with
-//   row(j) = row(c) + {j} (chain: j = c + 1) and token[j] = sampled[c] is.
+//   row(j) = row(c) + {j} (chain: j = c + 1) and token[j] = sampled[c] is.  Where slots
+//   are given, only nodes that have one, and a place of the path to be moved to.
 //
 // One warp to a request: its lanes look at 32 nodes at a time, the token first,
 // and the mask words only of those that have it.  Bound by latency: a few loads
@@ -60,18 +61,21 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
             }
             continue;
         }
-        int64_t c = 0, taken = nodes > 0 ? 1 : 0;
+        // (a request whose first node has no row keeps nothing)
+        const bool begins = nodes > 0 && !(p.slots && p.slots[lo] < 0);
+        int64_t c = 0, taken = begins ? 1 : 0;
         int32_t want = -1;
-        if (nodes > 0) {
+        if (begins) {
             want = p.sampled[lo];
             if (lane == 0) p.path[lo] = 0;
         }
-        while (nodes > 0 && want >= 0) {
+        while (begins && want >= 0) {
             int64_t found = -1;
             const int64_t upto = p.tree ? nodes : (c + 2 < nodes ? c + 2 : nodes);
             for (int64_t base = c + 1; base < upto && found < 0; base += 32) {
                 const int64_t j = base + lane;
-                const bool hit = j < upto && p.tokens[lo + j] == want && is_child(p, lo, nodes, c, j);
+                const bool hit = j < upto && p.tokens[lo + j] == want && is_child(p, lo, nodes, c, j) &&
+                                 !(p.slots && (p.slots[lo + j] < 0 || p.slots[lo + taken] < 0));
                 const uint32_t who = __ballot_sync(0xffffffffu, hit);
                 if (who) found = base + __ffs(who) - 1;
             }

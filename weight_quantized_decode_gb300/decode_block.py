@@ -81,11 +81,12 @@ class AttentionBlock:
         self.lens = self.lens.clone()
         self.lens[request] += len(path) - slots.numel()
 
-
     def accept(self, tokens, sampled, maps, tree=None):
         """After a tree step of all requests: the path that the tokens sampled at the nodes accept stays, for each of them,
-        as `keep` does it, but without a host read.  Returns TreeAccepted; its `next` are the next step's first tokens."""
-        got = qmv.qmv_tree_accept(tokens, sampled, maps.start, maps.kv_len, tree=tree)
+        as `keep` does it, but without a host read.  Where the step had no pages for some of a request's nodes (a device
+        status bit; `keep` refuses it) the path ends in front of them, and its length there; one whose first node had none
+        keeps the length it had, with a count of 0.  Returns TreeAccepted; its `next` are the next step's first tokens."""
+        got = qmv.qmv_tree_accept(tokens, sampled, maps.start, maps.kv_len, tree=tree, slots=maps.slots)
         qmv.qmv_kv_keep(self.cache, maps.slots, maps.start, got.path, got.count)
         self.lens = got.lens
         return got
