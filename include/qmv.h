@@ -575,7 +575,8 @@ QMV_API qmv_status qmv_sample(const void *logits, int64_t stride, int logits_f32
  *   start, kv_len, tree, tree_words : as for qmv_tree_attn.  A node that no row can
  *           name (past 32 * tree_words) is not accepted.
  *   path  : int32 [T]: at start[r] .., the accepted nodes (counted within the
- *           request) in order, then -1; -1 past start[R] too.
+ *           request) in order, then -1; -1 past start[R] too (where offsets fall:
+ *           past the last place that a request has).
  *   count, next, lens : int32 [R]: how many, the token drawn at the last of them
  *           (-1: none), and the length up to it, kv_len - (new tokens) + count.
  * A request whose offsets leave [0, T] or fall, or whose kv_len is below its new

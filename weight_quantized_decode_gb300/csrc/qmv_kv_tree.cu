@@ -92,10 +92,19 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const Accep
             p.lens[r] = static_cast<int32_t>(len - nodes + taken);
         }
     }
-    // Places past the last request's nodes: padding.
-    const int64_t end = p.R > 0 ? p.start[p.R] : 0;
-    if (end >= 0)
+    // Places past the last request's nodes are padding.  Where offsets fall, other requests' may lie there: past all of
+    // theirs.
+    const int64_t last = p.R > 0 ? p.start[p.R] : 0;
+    if (last >= 0 && last + first * 32 < p.T) {
+        int end = static_cast<int>(last);
+#pragma unroll 4
+        for (int64_t r = lane; r < p.R; r += 32) {
+            const int lo = p.start[r], hi = p.start[r + 1];
+            if (lo >= 0 && hi >= lo && hi <= p.T) end = max(end, hi);
+        }
+        end = __reduce_max_sync(0xffffffffu, end);
         for (int64_t i = end + first * 32 + lane; i < p.T; i += warps * 32) p.path[i] = -1;
+    }
 }
 
 // ---- kept rows --------------------------------------------------------------------
