@@ -85,7 +85,9 @@ class AttentionBlock:
         """After a tree step of all requests: the path that the tokens sampled at the nodes accept stays, for each of them,
         as `keep` does it, but without a host read.  Where the step had no pages for some of a request's nodes (a device
         status bit; `keep` refuses it) the path ends in front of them, and its length there; one whose first node had none
-        keeps the length it had, with a count of 0.  Returns TreeAccepted; its `next` are the next step's first tokens."""
+        keeps the length it had, with a count of 0.  Returns TreeAccepted; its `next` are the next step's first tokens, -1
+        for a request without one: nothing new in the step, no page for its first node, or nothing that could be drawn at the
+        last node of its path (logits that are -inf or no numbers, as where the attention met a missing page)."""
         got = qmv.qmv_tree_accept(tokens, sampled, maps.start, maps.kv_len, tree=tree, slots=maps.slots)
         qmv.qmv_kv_keep(self.cache, maps.slots, maps.start, got.path, got.count)
         self.lens = got.lens
@@ -93,16 +95,19 @@ class AttentionBlock:
 
 
 class Decoder:
-    """An embedding (fp16 [vocabulary, hidden]), an AttentionBlock and an output head (Q4_0 [vocabulary, hidden]): from
-    token ids to the next ones on the GPU."""
+    """An embedding (fp16 [vocabulary, hidden]), an AttentionBlock and an output head (Q4_0 [vocabulary, hidden], no more
+    tokens than the embedding): from token ids to the next ones on the GPU."""
 
     def __init__(self, block, embedding, head):
+        if head.numel() > embedding.shape[0] * (embedding.shape[1] // 32 * qmv.Q4_0_BLOCK_BYTES):
+            raise ValueError("Decoder: the head has more tokens than the embedding")
         self.block, self.embedding, self.head = block, embedding, head
 
     def logits(self, tokens, n_new, tree=None):
         """The requests' new tokens (int32 [T], as AttentionBlock.step takes them) through the model.  Returns (logits fp32
-        [T, vocabulary], maps)."""
-        x = self.embedding.index_select(0, tokens)
+        [T, vocabulary], maps).  A token of -1, none, is looked up as token 0: `next` of an earlier step can be given as it
+        is, but what a request without a token draws there means nothing (give it no new tokens, or finish it)."""
+        x = self.embedding.index_select(0, tokens.clamp(min=0))
         y, maps = self.block.step(x, n_new, tree)
         return self.block._product(self.head, (x + y).half()), maps
 
