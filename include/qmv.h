@@ -548,7 +548,8 @@ QMV_API qmv_status qmv_tree_attn(const void *q, int64_t q_stride, const void *k,
  *   temperature, top_p, min_p : fp32 [R], top_k : int32 [R]; for those that are NULL
  *            the number for all rows holds: of all[0], all[1], all[2] and top_k_all.
  *            all : HOST fp32 [3], read before the call returns (NULL: 1, 1, 0).
- *            0 or 2^-64 <= T <= 2^64, top_p >= 0, 0 <= min_p <= 1.
+ *            0 or 2^-64 <= T <= 2^64, top_p >= 0, 0 <= min_p <= 1 (a number of `all`
+ *            outside that holds for all rows: QMV_ERR_SHAPE).
  *   token  : int32 [R].  prob : fp32 [R] or NULL: w / sum of w of the token among
  *            those that stayed (T = 0: 1).
  * Logits of -inf are never drawn; a row of nothing else gives token -1 and prob 0.  A

@@ -873,6 +873,18 @@ def _setting(fn, name, value, rows, dtype, index):
     raise ValueError(f"{fn}: {name} must be a number or a contiguous {dtype} tensor of {rows}")
 
 
+def _sample_numbers(fn, t, p, m, k):
+    """The numbers for all rows as the call takes them: fp32 [3] and top_k.  The range is the fp32 number's, but a
+    temperature that only rounds to 0 is no request for the largest logit."""
+    try:
+        alike, top_k = (ctypes.c_float * 3)(t, p, m), int(k) if k == k and abs(k) != float("inf") else None
+    except OverflowError:
+        top_k = None
+    if top_k is None or k != top_k or not (t == 0 or 2.0 ** -64 <= alike[0] <= 2.0 ** 64) or not (p >= 0 and 0 <= m <= 1):
+        raise ValueError(f"{fn}: temperature must be 0 or 2^-64 .. 2^64, top_p not negative, min_p between 0 and 1, top_k whole")
+    return alike, max(-1, min(top_k, 1 << 19))
+
+
 def qmv_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
     """One token from each row of logits [R, V] (fp32 or fp16, dense rows any distance apart), by the uniform numbers u
     [R] (fp32, 0 <= u < 1).  temperature (0: the largest logit), top_k (0: all), top_p (1: all) and min_p (0: all): a
@@ -898,16 +910,14 @@ def qmv_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream
     k_ptr, k = _setting(fn, "top_k", top_k, R, torch.int32, at)
     p_ptr, p = _setting(fn, "top_p", top_p, R, torch.float32, at)
     m_ptr, m = _setting(fn, "min_p", min_p, R, torch.float32, at)
-    if not (t >= 0 and p >= 0 and 0 <= m <= 1) or k != int(k):
-        raise ValueError(f"{fn}: temperature and top_p must not be negative, min_p between 0 and 1, top_k whole")
+    alike, k = _sample_numbers(fn, t, p, m, k)
     device = logits.device
     if stream is None:
         token, prob = torch.empty(R, dtype=torch.int32, device=device), torch.empty(R, dtype=torch.float32, device=device)
     else:
         token, prob = (_output(R, t, device, at, stream) for t in (torch.int32, torch.float32))
     _call_on(fn, at, stream, (logits.data_ptr(), apart[0] if R > 1 else V, f32, u.data_ptr(), t_ptr, p_ptr, m_ptr,
-                              (ctypes.c_float * 3)(t, p, m), k_ptr, max(-1, min(int(k), V)), token.data_ptr(),
-                              prob.data_ptr(), R, V))
+                              alike, k_ptr, k, token.data_ptr(), prob.data_ptr(), R, V))
     return Sampled(token, prob)
 
 

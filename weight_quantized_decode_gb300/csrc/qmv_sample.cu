@@ -1101,6 +1101,10 @@ qmv_status qmv_sample(const void *logits, int64_t stride, int logits_f32, const 
 {
     if (R < 0 || R > (int64_t(1) << 26) || V < 1 || V > kSampleVocab || stride < 0 || stride > (int64_t(1) << 40))
         return QMV_ERR_SHAPE;
+    // (arrays of settings are checked row by row on the device)
+    if (all && ((!temperature && !(all[0] == 0.0f || (all[0] >= 0x1p-64f && all[0] <= 0x1p64f))) ||
+                (!top_p && !(all[1] >= 0.0f)) || (!min_p && !(all[2] >= 0.0f && all[2] <= 1.0f))))
+        return QMV_ERR_SHAPE;
     if (R == 0) return QMV_OK;
     if (!logits || !u || !token) return QMV_ERR_NULL;
     for (const void *a : {static_cast<const void *>(u), static_cast<const void *>(temperature),
