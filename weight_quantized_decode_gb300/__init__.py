@@ -39,6 +39,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 import threading
@@ -709,6 +710,16 @@ def rotary_axes(sections, turns=False):
     return bytes(i % k if i // k < sections[i % k] else 0 for i in range(n))
 
 
+def _axis_bytes(fn, axes):
+    """A byte to each pair, of whole numbers in any sequence, array or tensor of one dimension."""
+    if type(axes) is bytes:
+        return axes
+    try:
+        return bytes([operator.index(a) for a in (axes.tolist() if hasattr(axes, "tolist") else axes)])
+    except (TypeError, ValueError):
+        raise TypeError(f"{fn}: axes must be a sequence of whole numbers, one to a pair, 0 to 3") from None
+
+
 def _norm_weight(fn, name, w, heads, D, index):
     """(address, stride) of a norm's weights: [D], or [heads, D] with a row to each head."""
     one = w.dim() == 1
@@ -781,7 +792,7 @@ def qmv_kv_append(qkv, cache, slots, n_heads, pos=None, cos=None, sin=None, inte
                   cache.page, cache.page_stride))
         return q
     if axes is not None:
-        axes = axes if type(axes) is bytes else bytes(axes)
+        axes = _axis_bytes(fn, axes)
         if 2 * len(axes) != rot or (axes and max(axes) >= n_axes):
             raise ValueError(f"{fn}: axes must name one of pos's {n_axes} axes for each of the {rot // 2} pairs")
     q_w, q_apart = (0, 0) if q_norm is None else _norm_weight(fn, "q_norm", q_norm, n_heads, D, at)
