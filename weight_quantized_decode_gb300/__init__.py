@@ -701,13 +701,13 @@ def rotary_axes(sections, turns=False):
     """The axis that each pair of a rotation turns by, as qmv_kv_append takes it: sections[a] pairs of axis a, one
     section behind the other; turns: pair i belongs to axis i % len(sections) while that one has pairs left, the rest
     to axis 0 (which takes what the others leave)."""
-    sections, n = [int(s) for s in sections], sum(int(s) for s in sections)
+    sections = [int(s) for s in sections]
     if not 1 <= len(sections) <= 4 or min(sections) < 0:
         raise ValueError("rotary_axes: one to four sections, none negative")
     if not turns:
         return bytes(a for a, s in enumerate(sections) for _ in range(s))
     k = len(sections)
-    return bytes(i % k if i // k < sections[i % k] else 0 for i in range(n))
+    return bytes(i % k if i // k < sections[i % k] else 0 for i in range(sum(sections)))
 
 
 def _axis_bytes(fn, axes):
