@@ -189,8 +189,20 @@ def main() -> int:
     return drafted()
 
 
+def agree(truth, rows, said, seen, limit=1e-2):
+    """Whether two ways to the same tokens agree: truth[i] was drawn greedily from logits rows[i], said[i] from seen[i].  Rows
+    may be `limit` apart, relative to their norm, and two tokens may change places whose logits differ by less than the
+    rows do; behind such a pair the ways part, and no more is compared."""
+    for t, a, s, b in zip(truth, rows, said, seen):
+        if not float((a - b).norm()) <= limit * float(a.norm()):
+            return False
+        if t != s:
+            return float(a[t] - a[s]) <= 2 * float((a - b).abs().max())
+    return True
+
+
 def drafted() -> int:
-    """Drafted trees verified by their samples, beside the same tokens decoded one by one (on other product kernels, so
+    """Drafted trees verified by their samples, against the same tokens decoded one by one (on other product kernels, so
     that two nearly equal logits may change places)."""
     import torch
     hidden, heads, kv_heads, D, vocab = 2048, 16, 8, 128, 32000
@@ -204,28 +216,42 @@ def drafted() -> int:
                         embedding, head) for _ in range(2))
     count = lambda n: torch.tensor([n], dtype=torch.int32, device="cuda")  # noqa: E731
     prompt = torch.randint(0, vocab, (50,), generator=g, device="cuda", dtype=torch.int32)
-    greedy = dict(temperature=0.0)
-    zeros = torch.zeros(64, device="cuda")
+    greedy = lambda logits: qmv.qmv_sample(logits, torch.zeros(len(logits), device="cuda"), temperature=0.0).token  # noqa: E731
     # eight tokens, one at a time
-    drawn, _ = one.step(prompt, count(50), zeros[:50], **greedy)
-    truth = [int(drawn.token[-1])]
+    logits, _ = one.logits(prompt, count(50))
+    truth, rows = [int(greedy(logits)[-1])], [logits[-1]]
     for _ in range(8):
-        drawn, _ = one.step(count(truth[-1]), count(1), zeros[:1], **greedy)
-        truth.append(int(drawn.token[0]))
+        logits, _ = one.logits(count(truth[-1]), count(1))
+        truth.append(int(greedy(logits)[0]))
+        rows.append(logits[0])
     # the same by trees in which the draft is right for three tokens and then wrong
-    two.step(prompt, count(50), zeros[:50], **greedy)
-    mask = dev(tree_mask([-1, 0, 0, 1, 1, 4, 5, 2]))
-    said = [truth[0]]
+    logits, _ = two.logits(prompt, count(50))
+    said, seen, right = [int(greedy(logits)[-1])], [logits[-1]], True
+    parents = [-1, 0, 0, 1, 1, 4, 5, 2]
+    mask = dev(tree_mask(parents))
     while len(said) < 7:
-        t = truth[len(said) - 1:] + [0] * 4
-        nodes = torch.tensor([t[0], t[1], 1, 2, t[2], t[3], (t[4] + 1) % vocab, 3], dtype=torch.int32, device="cuda")
-        got = two.verify(nodes, count(8), zeros[:8], tree=mask, **greedy)
-        n = int(got.count[0])
-        said += [int(nodes[i]) for i in got.path[1:n].tolist()] + [int(got.next[0])]
-        print(f"tree of 8 nodes: {n} accepted, next token {int(got.next[0])}")
+        t = truth[len(said):] + [0] * 4
+        nodes = [said[-1], t[0], 1, 2, t[1], t[2], (t[3] + 1) % vocab, 3]
+        tokens = torch.tensor(nodes, dtype=torch.int32, device="cuda")
+        logits, maps = two.logits(tokens, count(8), mask)          # (what Decoder.verify does, logits in hand)
+        drawn = greedy(logits)
+        got = two.block.accept(tokens, drawn, maps, mask)
+        drew, path = drawn.tolist(), [0]
+        while True:
+            child = [j for j in range(8) if parents[j] == path[-1] and nodes[j] == drew[path[-1]]]
+            if not child:
+                break
+            path.append(child[0])
+        right = right and got.path.tolist() == path + [-1] * (8 - len(path)) and got.count.tolist() == [len(path)] and \
+            got.next.tolist() == [drew[path[-1]]]
+        said += [nodes[j] for j in path[1:]] + [drew[path[-1]]]
+        seen += [logits[j] for j in path]
+        print(f"tree of 8 nodes: {int(got.count[0])} accepted, next token {int(got.next[0])}")
     bad = qmv.qmv_device_status()
-    print(f"one by one {truth[:len(said)]}, by trees {said[:len(truth)]}, status {bad}")
-    return 1 if bad else 0
+    same = agree(truth, rows, said, seen)
+    print(f"one by one {truth[:len(said)]}, by trees {said[:len(truth)]}, {'agreed' if same else 'not the same'}, paths "
+          f"{'as drawn' if right else 'wrong'}, status {bad}")
+    return 0 if same and right and not bad else 1
 
 
 if __name__ == "__main__":
