@@ -80,7 +80,6 @@ struct PrefillParams {
     int NSA;           // weight-atom ring slots (tensor memory)
     int NSB;           // activation ring slots (shared memory)
     int KSUB;          // 64-K atoms per slot (1, 2 or 4): MMAs per barrier round = 4 * KSUB * WT
-    int cluster;       // CTAs per cluster sharing each activation tile by multicast (1 or 2)
     uint32_t tmem_cols;
     int test_skip_copy;   // failure-detection test only: CTA (0, 0) never requests its first packed tile
     unsigned long long *phase;   // phase-timeline builds only (QMV_PHASE_STAMPS): [count, records...]
@@ -116,25 +115,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
-}
-
-// tma_load_2d delivered to every CTA of `mask` in the cluster, at the same
-// shared-memory offsets (destination and barrier) in each.
-__device__ __forceinline__ void tma_load_2d_mc(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar,
-                                               uint16_t mask)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3}], [%4], %5;"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
 }
 
 // Every thread of every CTA of the cluster.
@@ -222,16 +202,6 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
-}
-
-// Arrive on the barrier at this offset in every CTA of `mask` once the MMAs
-// issued so far are complete.
-__device__ __forceinline__ void mma_commit_mc(uint64_t *bar, uint16_t mask)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(smem_u32(bar)), "h"(mask)
-        : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_32cols(uint32_t taddr, uint32_t (&v)[32])
@@ -362,9 +332,9 @@ __device__ __forceinline__ void st_cluster_f32x16(const float *local, uint32_t r
                      : "memory");
 }
 
-// SMALL: 16-token tiles (one weight tile, no multicast), which may be split
+// SMALL: 16-token tiles (one weight tile), which may be split
 // along K over a cluster; the other tiles compile without that code.
-template <int WT, int CL, int FMT, bool SMALL>
+template <int WT, int FMT, bool SMALL>
 __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    const PrefillParams p)
@@ -374,12 +344,9 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
     const int NW = p.NW, NSA = p.NSA, NSB = p.NSB, TN = p.TN, KSUB = p.KSUB;
-    // Equal ring depths without a cluster: one set of release barriers
-    // (aempty) serves both rings, and a slot is released with one commit.
-    const bool one_ring = NSA == NSB && CL == 1;
-    uint32_t crank = 0u;
-    if constexpr (CL > 1) crank = cluster_rank();
-    const uint16_t cmask = static_cast<uint16_t>((1u << CL) - 1u);
+    // Equal ring depths: one set of release barriers (aempty) serves both
+    // rings, and a slot is released with one commit.
+    const bool one_ring = NSA == NSB;
     const int b_atom_bytes = TN * kKB * 2;                  // one 64-K activation atom
     const int b_slot_bytes = KSUB * b_atom_bytes;
     // One weight row's 256-K chunk (144 bytes Q4_0, 272 Q8_0) and the TMA
@@ -397,8 +364,7 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
     uint64_t *afull = wempty + NW;      // [NSA] dequantised atoms written to tensor memory
     uint64_t *aempty = afull + NSA;     // [NSA] the slot's MMAs are done: its weight atoms are free
     uint64_t *bfull = aempty + NSA;     // [NSB] activation atoms landed
-    uint64_t *bempty = bfull + NSB;     // [NSB] every cluster CTA's MMAs of the slot are done: its
-                                        //       activation tile may be refilled in all of them
+    uint64_t *bempty = bfull + NSB;     // [NSB] the slot's MMAs are done: its activation tile may be refilled
     uint64_t *accfull = bempty + NSB;   // [1]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(accfull + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -435,7 +401,7 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
         }
         for (int i = 0; i < NSB; ++i) {
             mbar_init(&bfull[i], 1);
-            mbar_init(&bempty[i], CL);
+            mbar_init(&bempty[i], 1);
         }
         mbar_init(accfull, 1);
         *abort_flag = 0;
@@ -443,12 +409,7 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_slot, p.tmem_cols);
     tc_fence_before();
-    // The peer CTAs' barriers are initialised before any multicast copy or
-    // commit can reach them.
-    if constexpr (CL > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     // Columns [t * TN, (t + 1) * TN) hold weight tile t's accumulator; weight
@@ -497,13 +458,8 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
                 mbar_wait_bounded(&wfull[c % NW], (c / NW) & 1, nullptr);
     } else if (warp == kXProducerWarp) {
         // ---------------- activations: TMA tensor copies, one per atom ----------------
-        // With a cluster, this CTA loads rows [crank * TN / CL, ...) of every
-        // atom and multicasts them into the same offsets of all the cluster's
-        // CTAs; a slot is refilled once every CTA's MMAs have released it.
         // The whole warp runs the loop; one elected lane issues the copies.
         pdl_wait_prior_grid();
-        const int rows = TN / CL;
-        const int row_off_bytes = static_cast<int>(crank) * rows * 128;
         int issued = 0, s = 0;
         uint32_t phase = 1;
         for (int j = 0; j < nK; ++j) {
@@ -514,13 +470,9 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
             if (elect_one()) {
                 mbar_arrive_expect_tx(&bfull[s], b_slot_bytes);
                 for (int a = 0; a < KSUB; ++a) {
-                    uint8_t *dst = b_tiles + s * b_slot_bytes + a * b_atom_bytes + row_off_bytes;
+                    uint8_t *dst = b_tiles + s * b_slot_bytes + a * b_atom_bytes;
                     const int xk = ((SMALL ? c_first * (kKChunk / kKB) : 0) + j * KSUB + a) * kKB;
-                    if constexpr (CL > 1)
-                        tma_load_2d_mc(dst, &xmap, xk, static_cast<int>(m0) + static_cast<int>(crank) * rows,
-                                       &bfull[s], cmask);
-                    else
-                        tma_load_2d(dst, &xmap, xk, static_cast<int>(m0), &bfull[s]);
+                    tma_load_2d(dst, &xmap, xk, static_cast<int>(m0), &bfull[s]);
                 }
                 QMV_TRACE(j, 0);
             }
@@ -577,10 +529,7 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
                                         a_tmem + static_cast<uint32_t>((a * WT + t) * kAtomCols),
                                         b_desc + a * b_atom_step, idesc, j == 0 && a == 0);
                 mma_commit(&aempty[sa]);
-                if constexpr (CL > 1)
-                    mma_commit_mc(&bempty[sb], cmask);
-                else if (!one_ring)
-                    mma_commit(&bempty[sb]);
+                if (!one_ring) mma_commit(&bempty[sb]);
                 QMV_TRACE(j, 3);
             }
             __syncwarp();
@@ -1054,9 +1003,6 @@ __global__ void __launch_bounds__(SMALL ? kThreadsSmall : kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, p.tmem_cols);
     }
-    // No CTA leaves while a peer may still multicast into its shared memory or
-    // arrive on its barriers.
-    if constexpr (CL > 1) cluster_sync();
 #ifdef QMV_PHASE_STAMPS
     if (threadIdx.x == 0 && p.phase) {
         // the end stamp is taken before the record's slot is claimed: the
@@ -1105,11 +1051,11 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// Ring depths, cluster size and tile forced for tests and sweeps:
-// QMV_PREFILL_RING="NW,NS[,CL[,TN[,WT[,KSUB[,SK]]]]]" (packed-weight slots,
-// activation slots, CTAs per cluster, token tile, weight tiles per CTA, atoms
-// per slot, CTAs along K; NW below 1, NS below 2, CL other than 1 or 2, TN,
-// WT, KSUB or SK of 0 keep the rule).
+// Ring depths and tile forced for tests and sweeps:
+// QMV_PREFILL_RING="NW,NS[,-[,TN[,WT[,KSUB[,SK]]]]]" (packed-weight slots,
+// activation slots, a number that is not used, token tile, weight tiles per
+// CTA, atoms per slot, CTAs along K; NW below 1, NS below 2, TN, WT, KSUB or
+// SK of 0 keep the rule).
 int ring_override(int which)
 {
     static int v[7] = {0, 0, 0, 0, 0, 0, 0};
@@ -1146,8 +1092,8 @@ int max_active_clusters(int fmt, int sk, size_t smem)
         auto it = cache.find(key);
         if (it != cache.end()) return it->second;
     }
-    const void *k = fmt == kPfQ8_0 ? reinterpret_cast<const void *>(prefill_kernel<1, 1, kPfQ8_0, true>)
-                                   : reinterpret_cast<const void *>(prefill_kernel<1, 1, kPfQ4_0, true>);
+    const void *k = fmt == kPfQ8_0 ? reinterpret_cast<const void *>(prefill_kernel<1, kPfQ8_0, true>)
+                                   : reinterpret_cast<const void *>(prefill_kernel<1, kPfQ4_0, true>);
     int n = 0;
     if (ensure_smem_optin(k, smem) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
@@ -1175,8 +1121,8 @@ PrefillPlan prefill_plan(int64_t N, int64_t K, int64_t M, int sms, int fmt, int 
 {
     const int sk_force = ring_override(6);
     auto plan = [&](int sk) {
-        return plan_prefill(N, K, M, sms, ring_override(0), ring_override(1), ring_override(2), ring_override(3),
-                            ring_override(4), ring_override(5), fmt, sk);
+        return plan_prefill(N, K, M, sms, ring_override(0), ring_override(1), 0, ring_override(3), ring_override(4),
+                            ring_override(5), fmt, sk);
     };
     PrefillPlan pl = plan(sk_force > 0 ? sk_force : splitk);
     // An automatic split keeps every cluster of the grid resident at once.
@@ -1211,7 +1157,7 @@ cudaError_t launch_prefill(const PrefillPlan &pl, const void *W, const void *x, 
     {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(M)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K * 2)};
-        const cuuint32_t box[2] = {kKB, static_cast<cuuint32_t>(pl.TN / pl.cluster)};
+        const cuuint32_t box[2] = {kKB, static_cast<cuuint32_t>(pl.TN)};
         const cuuint32_t estr[2] = {1, 1};
         if (enc(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(x), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1230,7 +1176,6 @@ cudaError_t launch_prefill(const PrefillPlan &pl, const void *W, const void *x, 
     p.NSA = pl.NSA;
     p.NSB = pl.NSB;
     p.KSUB = pl.KSUB;
-    p.cluster = pl.cluster;
     p.tmem_cols = pl.tmem_cols;
     p.test_skip_copy = test_skip_copy ? 1 : 0;
 #ifdef QMV_PHASE_STAMPS
@@ -1241,20 +1186,17 @@ cudaError_t launch_prefill(const PrefillPlan &pl, const void *W, const void *x, 
         p.phase_seq = g_prefill_phase_seq.fetch_add(1);
     }
 #endif
-    // Q8_0 takes no multicast pairs (the plan never sets them for it).
-    if (q8 && pl.cluster > 1) return cudaErrorInvalidValue;
-    if (pl.splitk > 1 && (pl.cluster > 1 || pl.TN != 16)) return cudaErrorInvalidValue;
-    if (pl.TN == 16 && (pl.WT != 1 || pl.cluster != 1)) return cudaErrorInvalidValue;
+    if (pl.splitk > 1 && pl.TN != 16) return cudaErrorInvalidValue;
+    if (pl.TN == 16 && pl.WT != 1) return cudaErrorInvalidValue;
     auto kernel =
-        pl.TN == 16 ? (q8 ? prefill_kernel<1, 1, kPfQ8_0, true> : prefill_kernel<1, 1, kPfQ4_0, true>)
-        : q8 ? (pl.WT == 2 ? prefill_kernel<2, 1, kPfQ8_0, false> : prefill_kernel<1, 1, kPfQ8_0, false>)
-        : pl.WT == 2 ? (pl.cluster > 1 ? prefill_kernel<2, 2, kPfQ4_0, false> : prefill_kernel<2, 1, kPfQ4_0, false>)
-                     : (pl.cluster > 1 ? prefill_kernel<1, 2, kPfQ4_0, false> : prefill_kernel<1, 1, kPfQ4_0, false>);
+        pl.TN == 16 ? (q8 ? prefill_kernel<1, kPfQ8_0, true> : prefill_kernel<1, kPfQ4_0, true>)
+        : q8 ? (pl.WT == 2 ? prefill_kernel<2, kPfQ8_0, false> : prefill_kernel<1, kPfQ8_0, false>)
+             : (pl.WT == 2 ? prefill_kernel<2, kPfQ4_0, false> : prefill_kernel<1, kPfQ4_0, false>);
     cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(kernel), pl.smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(pl.grid_x), static_cast<unsigned>(pl.grid_y),
                     static_cast<unsigned>(pl.splitk));
-    const dim3 cluster(static_cast<unsigned>(pl.cluster), 1, static_cast<unsigned>(pl.splitk));
+    const dim3 cluster(1, 1, static_cast<unsigned>(pl.splitk));
     return launch_ex_cluster_dims(kernel, grid, dim3(pl.TN == 16 ? kThreadsSmall : kThreads), pl.smem, s, pdl,
                                   cluster, wmap, xmap, p);
 }

@@ -44,8 +44,7 @@ struct PrefillPlan {
     int NW;            // packed-weight ring slots (256-K chunks of WT tiles)
     int NSA;           // weight-atom ring slots in tensor memory
     int NSB;           // activation ring slots in shared memory
-    int cluster;       // CTAs per cluster along the weight tiles (1 or 2): each loads 1/cluster of every
-                       // activation tile and multicasts it to the others
+    static constexpr int cluster = 1;   // CTAs along the weight tiles that share activation tiles: none do
     uint32_t tmem_cols;   // allocated: WT accumulators [t * TN, (t + 1) * TN), then the weight atoms
     size_t smem;       // dynamic shared memory per CTA
     int64_t grid_x;    // CTAs along the weight rows (WT * 128 rows each)
@@ -90,17 +89,17 @@ inline int64_t prefill_cost(int64_t N, int64_t K, int64_t M, int sms, int TN, in
 // depth below 1 or an activation-ring depth below 2 keeps the rule; shared
 // memory and tensor memory still cap them).  One packed-weight slot is correct
 // (each dequantising thread copies its rows into registers before releasing
-// the slot) but slow.  cluster_force: 1 or 2 forces the cluster size;
-// tn_force (64..256, a multiple of 64) and wt_force (1 or 2) force the tile,
-// ksub_force (1, 2 or 4) the atoms per ring slot where tensor memory still
-// holds two weight-atom slots (0 keeps the rule).
+// the slot) but slow.  tn_force (64..256, a multiple of 64) and wt_force (1 or
+// 2) force the tile, ksub_force (1, 2 or 4) the atoms per ring slot where
+// tensor memory still holds two weight-atom slots (0 keeps the rule).  The
+// number before tn_force is not used.
 //
 // fmt: the packed weight format.  splitk: 0 = one CTA per tile along K;
 // -1 = as many CTAs along K (at most 8, at most one per 256-K chunk) as keep
 // the grid within one wave of `sms`; n > 0 forces n (tests and sweeps; kept
 // within the same limits).  Split K is taken with 16-token tiles only.
 inline PrefillPlan plan_prefill(int64_t N, int64_t K, int64_t M, int sms, int nw_force, int ns_force,
-                                int cluster_force = 0, int tn_force = 0, int wt_force = 0, int ksub_force = 0,
+                                int = 0, int tn_force = 0, int wt_force = 0, int ksub_force = 0,
                                 int fmt = kPfQ4_0, int splitk = 0)
 {
     PrefillPlan pl = {};
@@ -174,22 +173,14 @@ inline PrefillPlan plan_prefill(int64_t N, int64_t K, int64_t M, int sms, int nw
     pl.tmem_cols = kTmemCols;
     pl.smem = total();
     pl.grid_x = (N + 128 * WT - 1) / (128 * WT);
-    // Pairs of CTAs on neighbouring weight tiles can share every activation
-    // tile (cluster = 2): each brings in half of its token rows and multicasts
-    // them to both.  It halves the L2 reads and each SM's tensor-copy requests
-    // but measured slower (prefill workload 564 -> 509 TFLOP/s on the same
-    // GB300; the 512-token slice period 544 -> 608 ns), so the rule keeps one
-    // CTA per cluster; QMV_PREFILL_RING=",,2" forces pairs.  An odd tile count
-    // then gets one extra CTA whose rows lie past N (it loads zeros for its
-    // weights and stores nothing).
-    pl.cluster = 1;
-    if ((cluster_force == 1 || cluster_force == 2) && fmt == kPfQ4_0) pl.cluster = cluster_force;
-    pl.grid_x = (pl.grid_x + pl.cluster - 1) / pl.cluster * pl.cluster;
+    // Every CTA loads its own activation tiles.  (Pairs of CTAs on neighbouring
+    // weight tiles that share them, each bringing half to both, were measured
+    // slower: prefill workload 564 -> 509 TFLOP/s.)
     pl.grid_y = (M + TN - 1) / TN;
     // Split K: CTA z of the cluster adds rows [128 z / SK, 128 (z + 1) / SK) of
     // every CTA's partial tile, which the others store into its shared memory.
     const int64_t chunks = K / kKChunk;
-    if (splitk != 0 && TN == 16 && pl.cluster == 1) {
+    if (splitk != 0 && TN == 16) {
         int64_t sk = splitk > 0 ? splitk : 8;
         if (splitk < 0)
             while (sk > 1 && pl.grid_x * pl.grid_y * sk > sms) --sk;
