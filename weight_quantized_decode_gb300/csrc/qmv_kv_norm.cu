@@ -25,8 +25,10 @@ namespace {
 //
 // Bound by the bytes in fp32: 16381 tokens of 32 heads on 8 of 128 with norms and three
 // axes, fp16 cache, 613 MB in 100 us, 6.1 TB/s, 0.90 of the measured copy bandwidth.  fp16
-// rows in: 88 us for 60 of bytes; an 8-bit cache: 111 for 85: some 180 and 220 instructions to two
-// rows stand beside fewer bytes.  4099 tokens of 28 heads on 4, fp16, 16.8 us; one token 2.9.
+// rows in: 88 us for 60 of bytes; an 8-bit cache: 111 for 85.  There some 180 and 220 instructions to
+// two rows (fp16: 71 million, 61 us if every issue slot were used) stand beside fewer bytes, and fp16
+// rows have half the bytes under way that fp32 rows have.  4099 tokens of 28 heads on 4, fp16,
+// 16.8 us; one token 2.9.
 // Measured and not taken: rows through rings of asynchronous copies (107 to 145 us), 16
 // values to a lane (200), the norms' weights kept in registers (108 to 116).
 constexpr int kThreads = 128;
@@ -318,7 +320,9 @@ cudaError_t launch_kv_append_norm(NormAppendParams p, int D, bool x_f32, int kin
     const int per = 32 / (D / 8);
     const int groups = (p.a.Hq + 2 * p.a.Hkv + per - 1) / per;
     // Few tokens: their rows go to all the warps that the GPU holds.  Many: a warp takes whole tokens, so that it fetches a
-    // token's cosines once (16381 tokens, three axes: 153 us with 4 rows to a unit, 104 with 48).
+    // token's cosines once (16381 tokens, three axes: 153 us with 4 rows to a unit, 104 with 48).  The warps that run at
+    // once (4256 on 152 SMs) take a token each, and a few tokens more begin another wave: 48 heads, fp32 in, three axes,
+    // 2128 tokens 17 us, 2129 (a warp to each) 23, 4256 29, 4257 39, 8192 53, for 12, 12, 23, 23 and 45 of bytes.
     const int64_t share = kThreads / 32 * kBlocks * sms / p.a.T;
     p.units = static_cast<int>(share < 1 ? 1 : share > groups ? groups : share);
     int64_t g = (p.a.T * p.units + kThreads / 32 - 1) / (kThreads / 32);

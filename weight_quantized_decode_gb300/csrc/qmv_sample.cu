@@ -39,14 +39,17 @@ namespace cg = cooperative_groups;
 // A cluster of up to 16 CTAs holds the row in shared memory, a slice to each: the
 // logits are read once from memory, and what the steps exchange goes through
 // distributed shared memory.  Many rows, or longer ones, are read from memory again
-// instead, by clusters of one or two (qmv_sample_plan.h has both sides measured).
+// instead, by clusters of one to eight (qmv_sample_plan.h has both sides measured).
 //
-// Bound by instructions where rows are many (512 of 128256 unfiltered: 135 us for 39 of
-// bytes; the weights alone take 30 instructions to a token, on a pipeline that is busy
-// two thirds of the time; top-p 324, top-k 84, greedy 59), and by latencies where they
-// are few: one row with top-k and top-p 11 us, of which the logits' way into shared
-// memory is 1.6 and each of six barriers of the cluster 0.5 to 1; eight rows with top-p
-// 27 us (histogram 2.5, the bin it gives 2.5, weights 6, sorting 350 tokens 3).
+// Where rows are many, latency that nothing overlaps and instructions share the time (512
+// text-like rows of 128256, 39 us of bytes; in brackets the issue slots in use): greedy 59
+// (0.28: waits for loads and barriers; 1024 CTAs on 304 places are 3.4 waves), top-k 50 84
+// (0.35), unfiltered 135 (0.58: a token's weight takes 30 instructions), top-p 0.9 323
+// (0.65: the row is passed over three times).  Where they are few, a chain of latencies:
+// one row with top-k and top-p 11 us, of which the logits' way into shared memory is 1.6
+// and each of six barriers of the cluster 0.5 to 1; eight rows with top-p 28 us (barriers
+// 6, histogram 2.5, the bin it gives 2.5, weights 6, sorting 350 tokens 3, loads 1.6; the
+// rest is in none of these), and 39 where its instructions have to be fetched first.
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, kSampleBlocks) sample_kernel(const S
 
     if (p.reorder) {
         // Of kThreads neighbouring rows the ones with the most work come first: a row whose top-p takes all its tokens
-        // twice, begun last, would run alone (512 rows of 128256 with settings of their own: 203 us as they stand, 162 in
+        // twice, begun last, would run alone (512 rows of 128256 with settings of their own: 189 us as they stand, 153 in
         // this order).
         const int64_t first = r - r % kThreads, mine = first + tid;
         bool heavy = false;

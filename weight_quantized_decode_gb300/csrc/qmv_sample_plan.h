@@ -30,6 +30,8 @@ inline SamplePlan plan_sample(int64_t R, int64_t V, int sms)
     //      4 m            17/12/38     16/12/38     22/14/46     25/15/51     87/62/179     158/107/337   22/25/46     39/45/85
     //      2 m            25/14/57     26/14/58     26/15/61     34/17/75     81/45/167     136/85/290    17/15/34     31/29/65
     //      1 m            41/18/99     42/18/99     42/19/99     43/19/99     81/35/167     148/72/312    19/15/43     22/16/48
+    // (rows of normal logits times 1.7; text-like rows take longer with top-p: 512 of 128256 323 for 290.)  The rule knows
+    // rows and logits only: where all rows have top-k, one CTA to a row would be faster (512 x 128256: 72 for 85).
     // Rows of very different settings, more than run at once, end more evenly with two CTAs to a row (512 x 128256, each
     // row with settings of its own: 154 us, by one 266).
     const int64_t slots = static_cast<int64_t>(kSampleBlocks) * sms;
