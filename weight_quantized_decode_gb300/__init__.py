@@ -884,24 +884,27 @@ def _setting(fn, name, value, rows, dtype, index):
     raise ValueError(f"{fn}: {name} must be a number or a contiguous {dtype} tensor of {rows}")
 
 
+_three_floats = ctypes.c_float * 3
+
+
 def _sample_numbers(fn, t, p, m, k):
     """The numbers for all rows as the call takes them: fp32 [3] and top_k.  The range is the fp32 number's, but a
     temperature that only rounds to 0 is no request for the largest logit."""
     try:
-        alike, top_k = (ctypes.c_float * 3)(t, p, m), int(k) if k == k and abs(k) != float("inf") else None
-    except OverflowError:
+        alike, top_k = _three_floats(t, p, m), int(k)
+    except (OverflowError, ValueError):                  # (integers past any float; an infinite top_k or NaN)
         top_k = None
-    if top_k is None or k != top_k or not (t == 0 or 2.0 ** -64 <= alike[0] <= 2.0 ** 64) or not (p >= 0 and 0 <= m <= 1):
+    if top_k is None or k != top_k or not (p >= 0 and 0 <= m <= 1 and (t == 0 or 2.0 ** -64 <= alike[0] <= 2.0 ** 64)):
         raise ValueError(f"{fn}: temperature must be 0 or 2^-64 .. 2^64, top_p not negative, min_p between 0 and 1, top_k whole")
-    return alike, max(-1, min(top_k, 1 << 19))
+    return alike, top_k if -1 <= top_k <= 1 << 19 else -1 if top_k < 0 else 1 << 19
 
 
 def qmv_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
     """One token from each row of logits [R, V] (fp32 or fp16, dense rows any distance apart), by the uniform numbers u
-    [R] (fp32, 0 <= u < 1).  temperature (0: the largest logit), top_k (0: all), top_p (1: all) and min_p (0: all): a
-    number, or a tensor with one to a row (fp32; top_k int32).  The token is the lowest index at which the weights
-    exp((l - max l) / temperature) of the tokens that the filters left, summed in index order, pass u times their sum.
-    Returns Sampled."""
+    [R] (fp32, 0 <= u < 1).  temperature (0: the largest logit; else 2^-64 to 2^64), top_k (0: all), top_p (1: all) and
+    min_p (0: all): a number, or a tensor with one to a row (fp32; top_k int32; a row with one out of range gives -1).
+    The token is the lowest index at which the weights exp((l - max l) / temperature) of the tokens that the filters left,
+    summed in index order, pass u times their sum.  Returns Sampled."""
     torch = _torch()
     fn = "qmv_sample"
     at = logits.get_device()
